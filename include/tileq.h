@@ -339,6 +339,59 @@ tileq_status tileq_place_workspace_size(const tileq_place_in *in, size_t *bytes)
 tileq_status tileq_place_experts(const tileq_place_in *in, tileq_place_out *out, void *ws,
                                  size_t ws_bytes, tileq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Products with the experts' uncompressed weights, grouped by expert: the layer
+ * before TileQ compresses it, for calibration and comparison, for training, and
+ * for serving layers that stay in 16 or 8 bits.  (The pages have no counterpart:
+ * they start from trained weights.)
+ *
+ * The rows of x, y and their gradients are sorted by expert, as tileq_route's
+ * sorted_pairs orders them; expert e owns rows expert_offsets[e] ..
+ * expert_offsets[e+1] - 1, any number of them, none included:
+ *   tileq_grouped_gemm     y[p]  = W_e x[p]
+ *   tileq_grouped_gemm_dx  dx[p] = W_e^T dy[p]
+ *   tileq_grouped_gemm_dw  dW_e  = sum over the rows p of expert e of dy[p] x[p]^T
+ * Operands are bf16 or fp16, products are summed in fp32 and rounded once to
+ * out_dtype.  Rows outside [expert_offsets[0], expert_offsets[E]) belong to no
+ * expert: they are not read, and their output rows stay as they were.  dW is
+ * written for every expert (zeros where it has no rows).  Results are the same
+ * bits on every run.
+ *
+ * The offsets are read on the device, so a call can be captured into a graph
+ * and replayed with other routings.  Offsets outside [0, P] are cut to it and a
+ * falling pair counts as no rows, so no value of theirs leads out of the arrays;
+ * ranges that overlap give unspecified rows.
+ *
+ * ws: device workspace of at least TILEQ_GROUPED_WS_BYTES, zeroed once by the
+ * caller.  It holds the status word alone (tileq_device_status), which bounded
+ * device waits that give up write; calls may share it, also at the same time.
+ * ------------------------------------------------------------------------- */
+#define TILEQ_GROUPED_MAX_E 256
+#define TILEQ_GROUPED_WS_BYTES 256
+
+enum { TILEQ_DT_BF16 = 0, TILEQ_DT_F16 = 1, TILEQ_DT_F32 = 2, TILEQ_DT_E4M3 = 3 };
+
+typedef struct {
+  int dtype;        /* operands: TILEQ_DT_BF16 or TILEQ_DT_F16 (tileq_fp8_gemm: TILEQ_DT_E4M3) */
+  int out_dtype;    /* result: TILEQ_DT_BF16, TILEQ_DT_F16 or TILEQ_DT_F32 */
+  int E;            /* experts, 1..TILEQ_GROUPED_MAX_E */
+  int P;            /* rows of x and y, >= 0 */
+  int d_in, d_out;  /* any widths >= 1 whose strides are allowed */
+  /* Strides in elements, 0 = contiguous: rows of x / dx (ld_x), of y / dy
+   * (ld_y), rows and experts of W / dW [E, d_out, d_in] (ld_w, stride_w).
+   * Those of operands (not of the result) must be multiples of 16 bytes, and no
+   * less than a row (TILEQ_ERR_UNSUPPORTED / TILEQ_ERR_INVALID_ARG). */
+  int64_t ld_x, ld_y, ld_w, stride_w;
+  const int32_t *expert_offsets; /* device [E+1]; NULL with E = 1: every row is expert 0's */
+} tileq_grouped;
+
+tileq_status tileq_grouped_gemm(const tileq_grouped *g, const void *x, const void *w, void *y, void *ws,
+                                size_t ws_bytes, tileq_stream_t stream);
+tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const void *w, void *dx, void *ws,
+                                   size_t ws_bytes, tileq_stream_t stream);
+tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const void *dy, void *dw, void *ws,
+                                   size_t ws_bytes, tileq_stream_t stream);
+
 /* Synchronously read (and clear) the device status word in `ws`.
  * *status receives TILEQ_OK or the first device error recorded. */
 tileq_status tileq_device_status(void *ws, int *status, tileq_stream_t stream);

@@ -1,0 +1,238 @@
+"""The experts' grouped products on the GPU (forward, both gradients) against their definitions in 64 bits."""
+import pytest
+
+from experts_util import assert_within, offsets_of, ref_dw, ref_dx, ref_forward
+
+pytestmark = pytest.mark.gpu
+
+RAGGED = [0, 1, 15, 16, 17, 31, 32, 33, 0, 63, 64, 65, 127, 128, 129, 0]
+LONG = [255, 256, 257, 0, 300, 513, 1, 700]
+FEW = [0, 1, 0, 0, 2, 1, 0, 3]
+
+
+@pytest.fixture(scope="module")
+def tq():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import tiled_rank_b200 as tq
+    yield tq
+    assert tq.expert_status() == 0
+
+
+def _make(counts, d_in, d_out, dtype, first=0, behind=0, seed=0):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    off = offsets_of(counts, first, "cuda")
+    P, E = first + sum(counts) + behind, len(counts)
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device="cuda").to(dtype)
+    return rnd(P, d_in), rnd(P, d_out), rnd(E, d_out, d_in), off
+
+
+def _check_all(tq, x, dy, w, off, what):
+    y = tq.grouped_gemm(x, w, off)
+    dx = tq.grouped_gemm_dx(dy, w, off)
+    dw = tq.grouped_gemm_dw(x, dy, off)
+    assert tq.expert_status() == 0, what
+    a, b = int(off[0]), int(off[-1])
+    for name, got, (ref, mag), terms in (("y", y, ref_forward(x, w, off), w.shape[2]),
+                                         ("dx", dx, ref_dx(dy, w, off), w.shape[1])):
+        assert_within(got[a:b], ref[a:b], mag[a:b], terms, f"{what} {name}")
+    ref, mag = ref_dw(x, dy, off)
+    assert_within(dw, ref, mag, max(1, int((off[1:] - off[:-1]).max())), f"{what} dw")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("counts", [FEW, RAGGED, LONG, [1], [1000]], ids=["few", "ragged", "long", "one", "dense"])
+@pytest.mark.parametrize("d_in,d_out", [(256, 512), (1000, 696), (64, 16), (8, 8), (264, 1032)])
+def test_products(tq, counts, d_in, d_out, dtype):
+    import torch
+    x, dy, w, off = _make(counts, d_in, d_out, getattr(torch, dtype))
+    _check_all(tq, x, dy, w, off, f"{counts} {d_in} {d_out}")
+
+
+@pytest.mark.parametrize("E", [1, 60, 64, 256])
+def test_expert_counts(tq, E):
+    import torch
+    g = torch.Generator().manual_seed(E)
+    counts = torch.randint(0, 40, (E,), generator=g).tolist()
+    x, dy, w, off = _make(counts, 136, 200, torch.bfloat16)
+    _check_all(tq, x, dy, w, off, f"E={E}")
+
+
+@pytest.mark.parametrize("counts", [FEW, RAGGED, LONG], ids=["few", "ragged", "long"])
+def test_rows_of_no_expert_stay(tq, counts):
+    """Rows in front of the first and behind the last expert, NaN in the operands, keep what the output held."""
+    import torch
+    x, dy, w, off = _make(counts, 192, 320, torch.bfloat16, first=5, behind=70)
+    a, b = int(off[0]), int(off[-1])
+    for t in (x, dy):
+        t[:a] = float("nan")
+        t[b:] = float("nan")
+    for got in (tq.grouped_gemm(x, w, off, out=torch.full((x.shape[0], 320), 7.0, dtype=x.dtype, device="cuda")),
+                tq.grouped_gemm_dx(dy, w, off, out=torch.full((x.shape[0], 192), 7.0, dtype=x.dtype, device="cuda"))):
+        assert (got[:a] == 7).all() and (got[b:] == 7).all()
+        assert torch.isfinite(got[a:b]).all()
+    ref, mag = ref_dw(x, dy, off)
+    assert_within(tq.grouped_gemm_dw(x, dy, off), ref, mag, max(counts), "dw")
+
+
+def test_nan_stays_with_its_expert(tq):
+    """A row of NaN and infinities reaches its own row of y and dx and its own expert's dW alone."""
+    import torch
+    counts = [17, 33, 64, 1, 0, 130, 300]
+    x, dy, w, off = _make(counts, 256, 136, torch.bfloat16)
+    bad = int(off[2])                      # the row behind expert 1's last one
+    x[bad], dy[bad] = float("nan"), float("inf")
+    y, dx, dw = tq.grouped_gemm(x, w, off), tq.grouped_gemm_dx(dy, w, off), tq.grouped_gemm_dw(x, dy, off)
+    rest = torch.arange(x.shape[0], device="cuda") != bad
+    assert y[bad].isnan().all() and torch.isfinite(y[rest]).all()
+    assert (~torch.isfinite(dx[bad])).all() and torch.isfinite(dx[rest]).all()
+    assert dw[2].isnan().all() and torch.isfinite(dw[[0, 1, 3, 4, 5, 6]]).all()
+    assert (dw[4] == 0).all()
+
+
+@pytest.mark.parametrize("out_dtype", ["bfloat16", "float16", "float32"])
+def test_out_types_and_strides(tq, out_dtype):
+    """Operands and results inside larger arrays, odd result strides, every result type."""
+    import torch
+    out_dtype = getattr(torch, out_dtype)
+    counts = [40, 0, 3, 170]
+    P, E, I, O = sum(counts), 4, 100, 52
+    g = torch.Generator(device="cuda").manual_seed(3)
+    big = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 0.5).to(torch.bfloat16)  # noqa: E731
+    x, dy, w = big(P, 136)[:, 8:8 + I], big(P, 72)[:, 16:16 + O], big(E, 64, 120)[:, 3:3 + O, 8:8 + I]
+    off = offsets_of(counts, 0, "cuda")
+    y = torch.full((P, 67), 9.0, dtype=out_dtype, device="cuda")[:, :O]
+    dx = torch.full((P, 131), 9.0, dtype=out_dtype, device="cuda")[:, :I]
+    dw = torch.full((E, O + 3, 113), 9.0, dtype=out_dtype, device="cuda")
+    tq.grouped_gemm(x, w, off, out=y)
+    tq.grouped_gemm_dx(dy, w, off, out=dx)
+    tq.grouped_gemm_dw(x, dy, off, out=dw[:, :O, :I])
+    assert_within(y, *ref_forward(x, w, off), I, "y")
+    assert_within(dx, *ref_dx(dy, w, off), O, "dx")
+    assert_within(dw[:, :O, :I], *ref_dw(x, dy, off), 170, "dw")
+    assert (y._base[:, O:] == 9).all() and (dx._base[:, I:] == 9).all()
+    assert (dw[:, O:] == 9).all() and (dw[:, :, I:] == 9).all()
+
+
+def test_widths_without_a_multiple_of_anything(tq):
+    import torch
+    counts, I, O = [3, 90, 257], 37, 29
+    P = sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.float16)  # noqa: E731
+    x, dy, w = rnd(P, 40)[:, :I], rnd(P, 32)[:, :O], rnd(3, 29, 40)[:, :, :I]
+    _check_all(tq, x, dy, w, offsets_of(counts, 0, "cuda"), "odd widths")
+    # one row: its stride is not used, but the rows of w, 37 elements apart, cannot be a tensor map's
+    with pytest.raises(tq.TileQError):
+        tq.grouped_gemm(rnd(1, I), rnd(1, 2, I), offsets_of([1], 0, "cuda"))
+
+
+def test_no_rows(tq):
+    import torch
+    w = torch.ones(4, 24, 16, dtype=torch.bfloat16, device="cuda")
+    x, dy = w.new_empty(0, 16), w.new_empty(0, 24)
+    off = offsets_of([0, 0, 0, 0], 0, "cuda")
+    assert tq.grouped_gemm(x, w, off).shape == (0, 24) and tq.grouped_gemm_dx(dy, w, off).shape == (0, 16)
+    assert (tq.grouped_gemm_dw(x, dy, off) == 0).all()
+    # rows, but none of them an expert's
+    x, dy = w.new_ones(9, 16), w.new_ones(9, 24)
+    out = torch.full((9, 24), 3.0, dtype=w.dtype, device="cuda")
+    tq.grouped_gemm(x, w, off, out=out)
+    assert (out == 3).all() and (tq.grouped_gemm_dw(x, dy, off) == 0).all()
+
+
+def test_offsets_out_of_range_are_cut(tq):
+    """Bad offsets lead to no access outside the arrays: they are cut to [0, P], a falling pair is empty."""
+    import torch
+    x, dy, w, _ = _make([20, 20, 20], 64, 64, torch.bfloat16)
+    off = torch.tensor([-5, 20, 10, 4000], dtype=torch.int32, device="cuda")
+    y = tq.grouped_gemm(x, w, off)
+    cut = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    ref, mag = ref_forward(x, w[:1], cut)
+    assert_within(y[:10], ref[:10], mag[:10], 64, "y")       # rows 10..19 are in two ranges
+    dw = tq.grouped_gemm_dw(x, dy, off)
+    assert (dw[1] == 0).all()
+    ref, mag = ref_dw(x, dy, cut)
+    assert_within(dw[0], ref[0], mag[0], 20, "dw")
+    assert tq.expert_status() == 0
+
+
+def test_same_bits_every_time_and_in_a_graph(tq):
+    import torch
+    x, dy, w, off = _make(RAGGED, 512, 256, torch.bfloat16)
+    calls = [lambda **k: tq.grouped_gemm(x, w, off, **k), lambda **k: tq.grouped_gemm_dx(dy, w, off, **k),
+             lambda **k: tq.grouped_gemm_dw(x, dy, off, **k)]
+    want = [c() for c in calls]
+    for c, v in zip(calls, want):
+        assert torch.equal(c(), v)
+    outs = [torch.zeros_like(v) for v in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, o in zip(calls, outs):
+            c(out=o)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    # another routing of as many rows in the same graph
+    other = offsets_of(list(reversed(RAGGED)), 0, "cuda")
+    off.copy_(other)
+    graph.replay()
+    ref, mag = ref_forward(x, w, other)
+    assert_within(outs[0], ref, mag, 512, "replayed")
+    ref, mag = ref_dw(x, dy, other)
+    assert_within(outs[2], ref, mag, max(RAGGED), "replayed dw")
+
+
+def test_other_streams_at_the_same_time(tq):
+    import torch
+    a, b = _make(LONG, 256, 384, torch.bfloat16, seed=1), _make(FEW, 384, 256, torch.bfloat16, seed=2)
+    want = [tq.grouped_gemm(t[0], t[2], t[3]) for t in (a, b)]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, t in enumerate((a, b)):
+            got[i].append(tq.grouped_gemm(t[0], t[2], t[3], stream=s[i] if i else s[i].cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in got[i])
+
+
+def test_results_past_2_31_elements(tq):
+    """Output offsets that do not fit 32 bits: 70000 x 32768 results, the last rows checked."""
+    import torch
+    P, I, O = 70000, 64, 32768
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(P, I, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(2, O, I, generator=g, device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, P - 200, P], dtype=torch.int32, device="cuda")
+    y = tq.grouped_gemm(x, w, off)
+    at = torch.tensor([0, P - 201, P - 200, P - 1], device="cuda")
+    e = torch.tensor([0, 0, 1, 1], device="cuda")
+    for r, i in zip(at.tolist(), e.tolist()):
+        ref, mag = ref_forward(x[r:r + 1], w[i:i + 1], torch.tensor([0, 1]))
+        assert_within(y[r:r + 1], ref, mag, I, f"row {r}")
+
+
+def test_gradients_against_differences(tq):
+    """The gradients of sum(y * dy) along random directions against central differences of the forward.
+
+    The forward is bilinear, so a central difference is its derivative but for rounding: with fp32
+    results the sum over P * d_out values differs by less than 2^-23 * (d_in + P * d_out) of the
+    magnitudes' sum, far under the 1e-3 of the derivative's own scale that is asked for."""
+    import torch
+    counts, I, O = [30, 0, 100, 270], 64, 48
+    x, dy, w, off = _make(counts, I, O, torch.bfloat16, seed=7)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    # directions and steps that bf16 holds exactly: signs, and operands on a grid of 1/8
+    x, w = (x * 8).round().clamp(-16, 16) / 8, (w * 8).round().clamp(-16, 16) / 8
+    sign = lambda t: torch.randint(0, 2, t.shape, generator=g, device="cuda").mul_(2).sub_(1).to(t.dtype) / 8  # noqa: E731
+    vx, vw = sign(x), sign(w)
+    f = lambda a, b: (tq.grouped_gemm(a, b, off, out_dtype=torch.float32).double() * dy.double()).sum()  # noqa: E731
+    dx = tq.grouped_gemm_dx(dy, w, off, out_dtype=torch.float32).double()
+    dw = tq.grouped_gemm_dw(x, dy, off, out_dtype=torch.float32).double()
+    for num, ana, scale in (((f(x + vx, w) - f(x - vx, w)) / 2, (dx * vx.double()).sum(), (dx * vx.double()).norm()),
+                            ((f(x, w + vw) - f(x, w - vw)) / 2, (dw * vw.double()).sum(), (dw * vw.double()).norm())):
+        assert abs(num - ana) <= 1e-3 * scale, (num, ana, scale)

@@ -13,5 +13,22 @@ from ._lib import (  # noqa: F401
     tileq_workspace_size, tileq_set_stage_events, tileq_launch_count,
     tileq_wbig, tileq_sketch_workspace_size, tileq_sketch_lowrank,
     tileq_place_in, tileq_place_out, place_in, tileq_place_workspace_size, tileq_place_experts,
+    TILEQ_DT_BF16, TILEQ_DT_F16, TILEQ_DT_F32, TILEQ_DT_E4M3, tileq_grouped,
+    tileq_grouped_gemm, tileq_grouped_gemm_dx, tileq_grouped_gemm_dw,
 )
 from .layer import DeviceLayer  # noqa: F401
+
+# the products with the experts' uncompressed weights work on torch tensors: torch is imported with their first use
+_EXPERTS = ("expert_status", "grouped_gemm", "grouped_gemm_dw", "grouped_gemm_dx")
+
+
+def __getattr__(name):
+    if name in _EXPERTS:
+        from . import experts
+        globals().update({n: getattr(experts, n) for n in _EXPERTS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_EXPERTS])

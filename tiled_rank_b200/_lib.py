@@ -23,6 +23,12 @@ TILEQ_ERR_TIMEOUT = -5
 TILEQ_ERR_RANGE = -6
 TILEQ_LINEAR = 0
 TILEQ_SWIGLU = 1
+TILEQ_DT_BF16 = 0
+TILEQ_DT_F16 = 1
+TILEQ_DT_F32 = 2
+TILEQ_DT_E4M3 = 3
+TILEQ_GROUPED_MAX_E = 256
+TILEQ_GROUPED_WS_BYTES = 256
 TILEQ_ROUTE_TOPK_SOFTMAX = 0
 TILEQ_ROUTE_FULL_SOFTMAX = 1
 
@@ -34,6 +40,7 @@ EXPORTS = (
     "tileq_selftest_bounded_wait", "tileq_set_stage_events", "tileq_launch_count",
     "tileq_sketch_workspace_size", "tileq_sketch_lowrank",
     "tileq_place_workspace_size", "tileq_place_experts",
+    "tileq_grouped_gemm", "tileq_grouped_gemm_dx", "tileq_grouped_gemm_dw",
 )
 TILEQ_SKETCH_MAX_L = 160
 TILEQ_PLACE_MAX_R0 = 256
@@ -97,6 +104,15 @@ class tileq_per_expert_lr(ctypes.Structure):
     _fields_ = [("U_pe", ctypes.c_void_p * 3), ("V_pe", ctypes.c_void_p * 3)]
 
 
+class tileq_grouped(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("E", ctypes.c_int), ("P", ctypes.c_int),
+        ("d_in", ctypes.c_int), ("d_out", ctypes.c_int),
+        ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+        ("stride_w", ctypes.c_int64), ("expert_offsets", ctypes.c_void_p),
+    ]
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with `python -m tiled_rank_b200.build`")
@@ -124,6 +140,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tileq_sketch_lowrank": ([P(tileq_wbig), vp, c_int, c_int, vp, vp, vp, vp, c_size, vp], c_int),
         "tileq_place_workspace_size": ([P(tileq_place_in), P(c_size)], c_int),
         "tileq_place_experts": ([P(tileq_place_in), P(tileq_place_out), vp, c_size, vp], c_int),
+        "tileq_grouped_gemm": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
+        "tileq_grouped_gemm_dx": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
+        "tileq_grouped_gemm_dw": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
     }
     for name, (argtypes, restype) in sigs.items():
         fn = getattr(lib, name)
@@ -301,3 +320,20 @@ def tileq_place_experts(pin: tileq_place_in, grid_assign, ws, ideal=None, iterat
     _check(lib().tileq_place_experts(ctypes.byref(pin), ctypes.byref(out), _ptr(ws),
                                      ws.numel() * ws.element_size() if ws is not None else 0,
                                      _stream(stream)), "tileq_place_experts")
+
+
+def _grouped(name, g: tileq_grouped, a, b, out, ws, stream):
+    _check(getattr(lib(), name)(ctypes.byref(g), _ptr(a), _ptr(b), _ptr(out), _ptr(ws),
+                                ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)), name)
+
+
+def tileq_grouped_gemm(g: tileq_grouped, x, w, y, ws, stream=None):
+    _grouped("tileq_grouped_gemm", g, x, w, y, ws, stream)
+
+
+def tileq_grouped_gemm_dx(g: tileq_grouped, dy, w, dx, ws, stream=None):
+    _grouped("tileq_grouped_gemm_dx", g, dy, w, dx, ws, stream)
+
+
+def tileq_grouped_gemm_dw(g: tileq_grouped, x, dy, dw, ws, stream=None):
+    _grouped("tileq_grouped_gemm_dw", g, x, dy, dw, ws, stream)

@@ -1,0 +1,196 @@
+// C ABI of the experts' products (include/tileq.h): argument checks, tensor maps
+// and the choice of kernel.  The kernels are in grouped.cu.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "grouped.cuh"
+#include "kernels.cuh"
+
+namespace tileq {
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
+long long div_up(long long v, long long m) { return (v + m - 1) / m; }
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+struct Operand {
+  const void *base;
+  int dtype;
+  long long cols, rows, mats;  // extents, innermost first; mats == 0: a matrix
+  long long ld, stride;        // elements
+};
+
+// Tensor map with a box of 128 bytes x box_rows, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap *m, const Operand &o, int box_rows) {
+  const auto fn = encoder();
+  if (!fn) return false;
+  const int es = o.dtype == TILEQ_DT_E4M3 ? 1 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)std::max(o.rows, 1ll), (cuuint64_t)std::max(o.mats, 1ll)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(o.ld * es), (cuuint64_t)(o.stride * es)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType type = o.dtype == TILEQ_DT_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : o.dtype == TILEQ_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return fn(m, type, o.mats ? 3 : 2, const_cast<void *>(o.base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+// Strides of the call, contiguous where 0; those of one row or one expert are not used and made valid.
+struct Strides {
+  long long x, y, w, we;
+};
+tileq_status strides_of(const tileq_grouped *g, int es, bool w_is_result, Strides *s) {
+  const long long q = 16 / es;  // elements of 16 bytes
+  s->x = g->ld_x ? g->ld_x : g->d_in;
+  s->y = g->ld_y ? g->ld_y : g->d_out;
+  s->w = g->ld_w ? g->ld_w : g->d_in;
+  if (g->P <= 1) s->x = round_up(std::max<long long>(s->x, g->d_in), q), s->y = round_up(std::max<long long>(s->y, g->d_out), q);
+  if (s->x < g->d_in || s->y < g->d_out || s->w < g->d_in) return TILEQ_ERR_INVALID_ARG;
+  s->we = g->stride_w ? g->stride_w : s->w * g->d_out;
+  const long long matrix = (long long)(g->d_out - 1) * s->w + g->d_in;
+  if (g->E == 1) s->we = round_up(std::max(s->we, matrix), q);
+  if (s->we < matrix) return TILEQ_ERR_INVALID_ARG;
+  // what a tensor map can express
+  const long long most = (1ll << 40) - 16;
+  if (s->x * es > most || s->y * es > most || (!w_is_result && (s->w * es > most || s->we * es > most)))
+    return TILEQ_ERR_UNSUPPORTED;
+  return TILEQ_OK;
+}
+
+tileq_status check(const tileq_grouped *g, const void *a, const void *b, const void *out, const void *ws,
+                   size_t ws_bytes, bool fp8) {
+  if (!g || g->E < 1 || g->E > TILEQ_GROUPED_MAX_E || g->P < 0 || g->d_in < 1 || g->d_out < 1) return TILEQ_ERR_INVALID_ARG;
+  if (fp8 ? g->dtype != TILEQ_DT_E4M3 : g->dtype != TILEQ_DT_BF16 && g->dtype != TILEQ_DT_F16) return TILEQ_ERR_INVALID_ARG;
+  if (g->out_dtype != TILEQ_DT_BF16 && g->out_dtype != TILEQ_DT_F16 && g->out_dtype != TILEQ_DT_F32)
+    return TILEQ_ERR_INVALID_ARG;
+  if (g->ld_x < 0 || g->ld_y < 0 || g->ld_w < 0 || g->stride_w < 0) return TILEQ_ERR_INVALID_ARG;
+  if (!g->expert_offsets && g->E != 1) return TILEQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(g->expert_offsets) & 3) return TILEQ_ERR_INVALID_ARG;
+  if (!a || !b || !out || !aligned16(a) || !aligned16(b) || !aligned16(out)) return TILEQ_ERR_INVALID_ARG;
+  if (!ws) return TILEQ_ERR_INVALID_ARG;
+  if (ws_bytes < TILEQ_GROUPED_WS_BYTES) return TILEQ_ERR_WORKSPACE;
+  return TILEQ_OK;
+}
+
+// The wide kernel (pairs of CTAs, 256 x 256 tiles) needs experts with enough
+// rows to fill its columns; the narrow one (one CTA, 128 x 64) streams the
+// weights of experts with few rows.
+GroupedKernel pick(GroupedMode mode, const tileq_grouped *g) {
+  if (mode == GG_DW) return GG_WIDE;
+  const long long live = std::min(g->E, std::max(g->P, 1));
+  return g->P > 48 * live ? GG_WIDE : GG_NARROW;
+}
+
+tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const Operand &oa, const Operand &ob,
+                 bool fp8, cudaStream_t stream) {
+  const GroupedKernel k = pick(mode, g);
+  const int bn = grouped_tile_cols(k), lanes = grouped_tile_lanes(k), cg = lanes / 128;
+  a.offsets = g->expert_offsets;
+  a.E = g->E;
+  a.P = g->P;
+  a.bf16 = g->dtype == TILEQ_DT_BF16;
+  a.out_dtype = g->out_dtype;
+  a.nL = (int)div_up(a.L, lanes);
+  a.pair_store = g->out_dtype != TILEQ_DT_F32 && a.L % 2 == 0 && a.ldo % 2 == 0 && a.out_stride % 2 == 0;
+  const long long tiles = a.nL * (mode == GG_DW ? (long long)g->E * div_up(a.C, bn) : g->P / bn + std::min(g->E, g->P));
+  if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
+  if (!encode(&a.amap, oa, mode == GG_FWD ? 128 : 64) || !encode(&a.bmap, ob, mode == GG_DW ? 64 : 32))
+    return TILEQ_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms < cg) return TILEQ_ERR_CUDA;
+  const int grid = (int)std::min<long long>(sms / cg, tiles) * cg;
+  return launch_grouped(a, k, mode, fp8, grid, stream) == cudaSuccess ? TILEQ_OK : TILEQ_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace tileq
+
+using namespace tileq;
+
+extern "C" {
+
+tileq_status tileq_grouped_gemm(const tileq_grouped *g, const void *x, const void *w, void *y, void *ws,
+                                size_t ws_bytes, tileq_stream_t stream) {
+  const bool none = g && g->P == 0;  // nothing is read or written
+  tileq_status st = check(g, none ? w : x, w, none ? w : y, ws, ws_bytes, false);
+  if (st != TILEQ_OK) return st;
+  Strides s;
+  if ((st = strides_of(g, 2, false, &s)) != TILEQ_OK) return st;
+  if (s.x % 8 || s.w % 8 || s.we % 8) return TILEQ_ERR_UNSUPPORTED;
+  if (g->P == 0) return TILEQ_OK;
+  GroupedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.L = g->d_out;
+  a.R = g->d_in;
+  a.out = y;
+  a.ldo = s.y;
+  a.status = static_cast<int *>(ws);
+  return run(a, GG_FWD, g, {w, g->dtype, g->d_in, g->d_out, g->E, s.w, s.we}, {x, g->dtype, g->d_in, g->P, 0, s.x, 0},
+             false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const void *w, void *dx, void *ws,
+                                   size_t ws_bytes, tileq_stream_t stream) {
+  const bool none = g && g->P == 0;
+  tileq_status st = check(g, none ? w : dy, w, none ? w : dx, ws, ws_bytes, false);
+  if (st != TILEQ_OK) return st;
+  Strides s;
+  if ((st = strides_of(g, 2, false, &s)) != TILEQ_OK) return st;
+  if (s.y % 8 || s.w % 8 || s.we % 8) return TILEQ_ERR_UNSUPPORTED;
+  if (g->P == 0) return TILEQ_OK;
+  GroupedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.L = g->d_in;
+  a.R = g->d_out;
+  a.out = dx;
+  a.ldo = s.x;
+  a.status = static_cast<int *>(ws);
+  return run(a, GG_DX, g, {w, g->dtype, g->d_in, g->d_out, g->E, s.w, s.we}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0},
+             false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const void *dy, void *dw, void *ws,
+                                   size_t ws_bytes, tileq_stream_t stream) {
+  if (g && g->P == 0) x = dy = dw;  // zeros are written; the maps' base is never read
+  tileq_status st = check(g, x, dy, dw, ws, ws_bytes, false);
+  if (st != TILEQ_OK) return st;
+  Strides s;
+  if ((st = strides_of(g, 2, true, &s)) != TILEQ_OK) return st;
+  if (s.x % 8 || s.y % 8) return TILEQ_ERR_UNSUPPORTED;
+  GroupedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.L = g->d_in;
+  a.C = g->d_out;
+  a.out = dw;
+  a.ldo = s.w;
+  a.out_stride = s.we;
+  a.status = static_cast<int *>(ws);
+  return run(a, GG_DW, g, {x, g->dtype, g->d_in, g->P, 0, s.x, 0}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0}, false,
+             reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

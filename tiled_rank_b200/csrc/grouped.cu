@@ -1,0 +1,518 @@
+// The experts' grouped products on the 5th-generation tensor cores: forward,
+// gradient of the rows, gradient of the weights (GroupedMode), and the forward
+// of e4m3 operands with a scale for every 128 of the reduction.  Rows are sorted
+// by expert; expert e owns rows offsets[e] .. offsets[e + 1], read on the device.
+//
+// All three are one tile product with the roles of the operands exchanged:
+//   out[c][l] = sum_r A[l][r] B[c][r]
+// l, the output's contiguous dimension, lies on the 128 TMEM lanes of a CTA and
+// c, its rows, on the TMEM columns:
+//   GG_FWD  A = W[e]   (r contiguous)   B = x rows  (r contiguous)   r: d_in
+//   GG_DX   A = W[e]^T (l contiguous)   B = dy rows (r contiguous)   r: d_out
+//   GG_DW   A = x^T    (l contiguous)   B = dy^T    (c contiguous)   r: rows of e
+// Weights on the lanes, so that the ragged dimension (the rows of an expert) is
+// the MMA's N, which takes any multiple of 16 or 32 at run time: a short last
+// tile costs its own columns only.  The epilogue stores a column's 32 lanes as
+// one 64- or 128-byte run of an output row in every mode.
+//
+// One persistent CTA per SM (CG = 1) or a pair of CTAs on neighbouring SMs that
+// share one MMA of 256 lanes (CG = 2: each CTA loads its own 128 rows of A and
+// half of B's, so an SM reads 32 KB per 64-element step of a 256 x 256 tile
+// instead of 48 KB).  Warps of a CTA:
+//   0      producer: TMA tiles (128-byte swizzle) of one 128-byte reduction step
+//          per stage into a ring; in GG_DW it also zeroes the rows of the next
+//          expert in the last step (both operands: 0 * NaN would be NaN);
+//   1      MMA issuer (first CTA of a pair): four MMAs per stage into an fp32
+//          TMEM accumulator, two or four accumulators in turn;
+//   2      the table of the experts' rows and tiles, before the others start;
+//   4..    epilogue: TMEM to registers, one rounding, stores.
+// fp8: one 128-byte stage is one scale block.  Every block gets an accumulator
+// of its own, which the epilogue warps fold into fp32 registers with
+// xs[block][row] * ws[e][l / 128][block]: one FMA per product of sums, as the
+// scales are no powers of two in general and cannot be left to the exponent.
+// Every wait is bounded and reports TILEQ_ERR_TIMEOUT.
+#include "grouped.cuh"
+
+#include <atomic>
+
+#include "kernels.cuh"
+#include "tc_pair.cuh"
+
+namespace tileq {
+namespace {
+
+constexpr int kBoxRows = 32;        // rows of one box of a row operand (B of GG_FWD, GG_DX)
+constexpr int kFirstEpw = 4;        // first epilogue warp
+constexpr int kRegsControl = 56, kRegsEpilogue = 224;  // registers a thread where the warps split them
+constexpr int kRowTileGroup = 8;    // column tiles that share a pass over the lane tiles
+
+template <int CG_, int BN_, bool F8_>
+struct GCfg {
+  static constexpr int CG = CG_, BN = BN_;
+  static constexpr bool F8 = F8_;
+  static constexpr int LANES = 128 * CG;
+  static constexpr int KE = F8 ? 128 : 64;  // reduction elements per stage (128 bytes)
+  static constexpr int EPW = BN == 256 ? 8 : 4;
+  static constexpr int COLS = BN / (EPW / 4);  // columns of one epilogue warp
+  static constexpr int THREADS = (kFirstEpw + EPW) * 32;
+  static constexpr bool SPLIT_REGS = F8 && BN == 256;
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = BN / CG * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int SQ = 200 * 1024 / STAGE;
+  static constexpr int NACC = BN == 256 ? 2 : 4;
+  static constexpr int TMEM_COLS = NACC * BN;
+  static constexpr int BAR_OFF = SQ * STAGE;
+  static constexpr int SCALE_OFF = BAR_OFF + (2 * SQ + 2 * NACC + 2) * 8 + 16;
+  static constexpr int TAB_OFF = SCALE_OFF + (F8 ? 2 * BN * 4 : 0);
+  static constexpr int SMEM = TAB_OFF + (3 * kGroupedMaxE + 1) * 4 + 1024;
+  static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two of tensor memory columns");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct Tile {
+  int e, row0, rows;  // expert and its rows
+  int l0, c0, ncols;  // first lane of the tile, first column, columns
+};
+
+// The tiles of the call, experts in order; first[e] = tiles before expert e.
+// Within an expert the column tiles go in groups that share a pass over the lane
+// tiles, so that the CTAs at work read few distinct rows of either operand.
+template <class G, GroupedMode MODE>
+struct Tiles {
+  const int *first, *beg, *cnt;
+  int E, L, nL, C, e = 0;
+  __device__ bool get(int w, Tile &t) {
+    if (w >= first[E]) return false;
+    while (w >= first[e + 1]) ++e;
+    const int i = w - first[e], total = MODE == GG_DW ? C : cnt[e];
+    const int nc = (total + G::BN - 1) / G::BN;
+    const int grp = i / (kRowTileGroup * nL), rem = i - grp * kRowTileGroup * nL;
+    const int gsz = min(kRowTileGroup, nc - grp * kRowTileGroup);
+    const int l = rem / gsz, c = grp * kRowTileGroup + rem % gsz;
+    // equal tiles, rounded to the MMA's step: one short tile would leave its CTAs idle
+    const int step = 16 * G::CG, tc = ((total + nc - 1) / nc + step - 1) / step * step;
+    t.e = e;
+    t.row0 = beg[e];
+    t.rows = cnt[e];
+    t.l0 = l * G::LANES;
+    t.c0 = c * tc;
+    t.ncols = min(tc, total - t.c0);
+    return true;
+  }
+};
+
+// 32 lanes x 16 columns into r; the values are there after wait16 of the same r.
+__device__ __forceinline__ void wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// mbar_wait by a whole warp with one answer: no lane leaves a loop in which the others still meet.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status) {
+  return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, status));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype) {
+  if (dtype == TILEQ_DT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return h2_as_u32(__floats2half2_rn(lo, hi));
+}
+
+// Columns c .. c + 15 of this warp's 32 lanes (l: this thread's) to out + column * ldo + l.
+__device__ __forceinline__ void store16(const GroupedArgs &P, long long base, int c, int ncols, int l, int lane,
+                                        const float (&v)[16]) {
+  if (P.out_dtype == TILEQ_DT_F32) {
+    float *out = reinterpret_cast<float *>(P.out) + base + l;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < ncols && l < P.L) out[(long long)(c + i) * P.ldo] = v[i];
+  } else if (P.pair_store) {
+    // lanes 2j and 2j + 1 exchange so that each stores two neighbouring outputs of one column
+    const int odd = lane & 1;
+    uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base + (l & ~1);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+      const uint32_t w = odd ? pack2(got, v[i + 1], P.out_dtype) : pack2(v[i], got, P.out_dtype);
+      if (c + i + odd < ncols && l < P.L)
+        *reinterpret_cast<uint32_t *>(out + (long long)(c + i + odd) * P.ldo) = w;
+    }
+  } else {
+    uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base + l;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < ncols && l < P.L) out[(long long)(c + i) * P.ldo] = (uint16_t)pack2(v[i], 0.f, P.out_dtype);
+  }
+}
+
+template <class G, GroupedMode MODE>
+__global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_constant__ GroupedArgs P) {
+  constexpr int CG = G::CG, SQ = G::SQ, NACC = G::NACC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF);
+  uint64_t *empty = full + SQ;
+  uint64_t *acc_full = empty + SQ;
+  uint64_t *acc_empty = acc_full + NACC;
+  uint64_t *tail = acc_empty + NACC;  // GG_DW: the copies of a step with foreign rows
+  uint64_t *drain = tail + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  float *scale = reinterpret_cast<float *>(smem + G::SCALE_OFF);
+  int *first = reinterpret_cast<int *>(smem + G::TAB_OFF), *beg = first + kGroupedMaxE + 1, *cnt = beg + kGroupedMaxE;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : tc::cluster_rank();
+  const int unit0 = blockIdx.x / CG, units = gridDim.x / CG;
+  auto stage_a = [&](int s) { return smem + s * G::STAGE; };
+  auto stage_b = [&](int s) { return smem + s * G::STAGE + G::A_BYTES; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SQ; ++s) {
+      mbar_init(&full[s], CG);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], G::EPW * CG);
+    }
+    mbar_init(tail, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tc::alloc_cg<CG>(tmem_slot, G::TMEM_COLS);
+  // the prologue overlaps the previous kernel's tail
+  pdl_wait_and_release();
+  if (warp == 2) {
+    // rows and tiles of each expert; offsets outside [0, P] or falling ones are cut to what is in range
+    int before = 0;
+    for (int e0 = 0; e0 < P.E; e0 += 32) {
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < P.E) {
+        const int lo = P.offsets ? min(max(P.offsets[e], 0), P.P) : 0;
+        const int hi = P.offsets ? min(max(P.offsets[e + 1], lo), P.P) : P.P;
+        beg[e] = lo;
+        cnt[e] = hi - lo;
+        n = P.nL * (((MODE == GG_DW ? P.C : hi - lo) + G::BN - 1) / G::BN);
+      }
+      int sum = n;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (e < P.E) first[e + 1] = before + sum;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) first[0] = 0;
+  }
+  tc::fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) tc::cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Tiles<G, MODE> tiles{first, beg, cnt, P.E, P.L, P.nL, P.C};
+  auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
+  // columns of the tile's MMA
+  auto mma_n = [&](const Tile &t) { return (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG); };
+  Tile t;
+  bool ok = true;
+
+  if constexpr (G::SPLIT_REGS) {
+    if (warp < kFirstEpw) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsControl));
+  }
+  if (warp == 0) {
+    // ============================================================ producer
+    uint32_t qi = 0, tails = 0;
+    for (int w = unit0; ok && tiles.get(w, t); w += units) {
+      const int nk = steps(t), half = mma_n(t) / CG;
+      const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
+      constexpr int BBOX = MODE == GG_DW ? 64 : kBoxRows;  // columns of one box of B
+      const int nbox = (half + BBOX - 1) / BBOX;
+      const uint32_t bytes = G::A_BYTES + nbox * BBOX * 128;
+      for (int kb = 0; kb < nk; ++kb, ++qi) {
+        const int s = qi % SQ;
+        const int left = MODE == GG_DW ? t.rows - kb * G::KE : G::KE;
+        const bool cut = left < G::KE && (left & 15);  // the last MMA of the step reaches the next expert's rows
+        if (qi >= (uint32_t)SQ && !(ok = warp_wait(&empty[s], ((qi / SQ) - 1) & 1, P.status))) break;
+        if (lane == 0) {
+          uint32_t bar = smem_addr(&full[s]);
+          if (cut) {
+            bar = smem_addr(tail);
+            mbar_arrive_expect_tx(tail, bytes);
+          } else if (CG == 2) {
+            bar = tc::map_cta(&full[s], 0);
+            tc::arrive_expect_at(bar, bytes);
+          } else {
+            mbar_arrive_expect_tx(&full[s], bytes);
+          }
+          uint8_t *a = stage_a(s), *b = stage_b(s);
+          if constexpr (MODE == GG_FWD) {
+            tc::tma_3d<CG>(a, &P.amap, kb * G::KE, l0, t.e, bar);
+          } else if constexpr (MODE == GG_DX) {
+            tc::tma_3d<CG>(a, &P.amap, l0, kb * 64, t.e, bar);
+            tc::tma_3d<CG>(a + 8192, &P.amap, l0 + 64, kb * 64, t.e, bar);
+          } else {
+            tc::tma_2d<CG>(a, &P.amap, l0, t.row0 + kb * 64, bar);
+            tc::tma_2d<CG>(a + 8192, &P.amap, l0 + 64, t.row0 + kb * 64, bar);
+          }
+          for (int i = 0; i < nbox; ++i) {
+            if constexpr (MODE == GG_DW)
+              tc::tma_2d<CG>(b + i * 8192, &P.bmap, c0 + i * 64, t.row0 + kb * 64, bar);
+            else
+              tc::tma_2d<CG>(b + i * kBoxRows * 128, &P.bmap, kb * G::KE, t.row0 + c0 + i * kBoxRows, bar);
+          }
+        }
+        if (cut) {
+          __syncwarp();
+          if (!(ok = warp_wait(tail, tails++ & 1, P.status))) break;
+          const int to = (left + 15) & ~15;
+          for (int i = lane; i < (to - left) * 8; i += 32) {
+            const int off = (left + i / 8) * 128 + (i % 8) * 16;  // whole rows: the swizzle stays inside a row
+            for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4 *>(stage_a(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < nbox; ++j)
+              *reinterpret_cast<uint4 *>(stage_b(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::arrive_at(tc::map_cta(&full[s], 0));
+        }
+      }
+    }
+    // no copy of this CTA may land and no commit may arrive after it has gone
+    if (lane == 0)
+      for (uint32_t i = qi > (uint32_t)SQ ? qi - SQ : 0; ok && i < qi; ++i)
+        ok = mbar_wait(&empty[i % SQ], (i / SQ) & 1, P.status);
+    if (lane == 0 && !ok && rank == 0)
+      for (uint32_t i = qi > (uint32_t)SQ ? qi - SQ : 0; i < qi; ++i) mbar_wait(&full[i % SQ], (i / SQ) & 1, P.status);
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    if (rank == 0) {
+      constexpr bool A_MN = MODE != GG_FWD, B_MN = MODE == GG_DW;  // output dimension contiguous
+      const uint32_t fmt = P.bf16 && !G::F8 ? (1u << 7) | (1u << 10) : 0u;
+      uint32_t qi = 0, ai = 0;
+      for (int w = unit0; ok && tiles.get(w, t); w += units) {
+        const int nk = steps(t);
+        if (nk == 0) continue;
+        const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+                               ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
+        for (int kb = 0; kb < nk; ++kb, ++qi) {
+          const int s = qi % SQ, ab = ai % NACC;
+          if ((G::F8 || kb == 0) && ai >= (uint32_t)NACC &&
+              !(ok = warp_wait(&acc_empty[ab], ((ai / NACC) - 1) & 1, P.status)))
+            break;
+          if (!(ok = warp_wait(&full[s], (qi / SQ) & 1, P.status))) break;
+          tc::fence_after();
+          // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
+          const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
+          const uint64_t ad = tc::sdesc(smem_addr(stage_a(s)), A_MN ? 8192 : 16);
+          const uint64_t bd = tc::sdesc(smem_addr(stage_b(s)), B_MN ? 8192 : 16);
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (MODE != GG_DW || kk < nmma)
+                tc::mma_ss<CG, G::F8>(tmem + ab * G::BN, ad + (uint64_t)(kk * (A_MN ? 128 : 2)),
+                                      bd + (uint64_t)(kk * (B_MN ? 128 : 2)), idesc,
+                                      (kk || (!G::F8 && kb)) ? 1u : 0u);
+            tc::commit_cg<CG>(&empty[s]);
+            if (G::F8 || kb == nk - 1) tc::commit_cg<CG>(&acc_full[ab]);
+          }
+          __syncwarp();
+          if (G::F8 || kb == nk - 1) ++ai;
+        }
+      }
+      // all issued MMAs have retired before tensor memory is released
+      if (tc::elect_one()) tc::commit_cg<CG>(drain);
+      __syncwarp();
+      warp_wait(drain, 0, P.status);
+    }
+  } else if (warp >= kFirstEpw) {
+    // ============================================================ epilogue
+    // 128 accumulators a thread: the register file has room for them once the first four warps give theirs up
+    // (168 registers a thread at launch: 384 * 168 = 128 * (56 + 2 * 224))
+    if constexpr (G::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsEpilogue));
+    const int half = (warp - kFirstEpw) >> 2;
+    const int row = (warp & 3) * 32 + lane;  // TMEM lane quadrant of this warp
+    const uint32_t lane_addr = tc::lane_base(warp);
+    uint32_t ai = 0;
+    // (fp8: the four warps of a named barrier stay together, also after a wait that gave up)
+    for (int w = unit0; (ok || G::F8) && tiles.get(w, t); w += units) {
+      const int nk = steps(t), l = t.l0 + (int)rank * 128 + row;
+      const long long base = MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)t.c0 * P.ldo
+                                           : (long long)(t.row0 + t.c0) * P.ldo;
+      const int cw = half * G::COLS;  // first column of this warp
+      if constexpr (!G::F8) {
+        const int ab = ai % NACC;
+        if (nk > 0) {
+          if (!(ok = warp_wait(&acc_full[ab], (ai / NACC) & 1, P.status))) break;
+          tc::fence_after();
+        }
+#pragma unroll 1
+        for (int c = cw; c < min(cw + G::COLS, t.ncols); c += 32) {
+          uint32_t r[2][16];
+          if (nk > 0) {
+            tc::ld16_nowait(tmem + lane_addr + ab * G::BN + c, r[0]);
+            tc::ld16_nowait(tmem + lane_addr + ab * G::BN + c + 16, r[1]);
+            wait16(r[0]);
+            wait16(r[1]);
+          }
+          float v[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = nk > 0 ? __uint_as_float(r[h][i]) : 0.f;  // an expert without rows
+            store16(P, base, c + 16 * h, t.ncols, l, lane, v);
+          }
+        }
+        if (nk > 0) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::arrive_at(tc::map_cta(&acc_empty[ab], 0));
+          ++ai;
+        }
+      } else {
+        float acc[G::COLS];
+#pragma unroll
+        for (int i = 0; i < G::COLS; ++i) acc[i] = 0.f;
+        const int tid = threadIdx.x & 127;  // within the four warps that share these columns
+        const bool has = tid < G::COLS && cw + tid < t.ncols;
+        const float *xs = P.xs + t.row0 + t.c0 + cw + tid;
+        const float *ws = P.ws + ((long long)t.e * P.nLb + min((t.l0 + (int)rank * 128) / 128, P.nLb - 1)) * P.nKb;
+        float sx = has ? __ldg(xs) : 0.f, sw = __ldg(ws);
+        for (int kb = 0; kb < nk; ++kb, ++ai) {
+          const int ab = ai % NACC;
+          float *sc = scale + (ai & 1) * G::BN + cw;
+          if (tid < G::COLS) sc[tid] = sx * sw;
+          if (kb + 1 < nk) {
+            sx = has ? __ldg(xs + (long long)(kb + 1) * P.ld_xs) : 0.f;
+            sw = __ldg(ws + kb + 1);
+          }
+          // also keeps these warps within one block of each other: two scale buffers do
+          named_sync(1 + half, 128);
+          ok = ok && warp_wait(&acc_full[ab], (ai / NACC) & 1, P.status);
+          tc::fence_after();
+          const uint32_t ta = tmem + lane_addr + ab * G::BN + cw;
+          constexpr int NCH = G::COLS / 16;
+          uint32_t r[2][16];
+          if (cw < t.ncols) {
+            tc::ld16_nowait(ta, r[0]);
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+              if (cw + ch * 16 < t.ncols) {
+                wait16(r[ch & 1]);
+                if (ch + 1 < NCH && cw + (ch + 1) * 16 < t.ncols) tc::ld16_nowait(ta + (ch + 1) * 16, r[(ch + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                  const float4 f = *reinterpret_cast<const float4 *>(sc + ch * 16 + i);
+                  acc[ch * 16 + i] = fmaf(__uint_as_float(r[ch & 1][i]), f.x, acc[ch * 16 + i]);
+                  acc[ch * 16 + i + 1] = fmaf(__uint_as_float(r[ch & 1][i + 1]), f.y, acc[ch * 16 + i + 1]);
+                  acc[ch * 16 + i + 2] = fmaf(__uint_as_float(r[ch & 1][i + 2]), f.z, acc[ch * 16 + i + 2]);
+                  acc[ch * 16 + i + 3] = fmaf(__uint_as_float(r[ch & 1][i + 3]), f.w, acc[ch * 16 + i + 3]);
+                }
+              }
+            }
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::arrive_at(tc::map_cta(&acc_empty[ab], 0));
+        }
+#pragma unroll
+        for (int ch = 0; ch < G::COLS / 16; ++ch) {
+          if (ok && cw + ch * 16 < t.ncols) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = acc[ch * 16 + i];
+            store16(P, base, cw + ch * 16, t.ncols, l, lane, v);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) {
+    // the last commit arrives in both CTAs; only here, where it is due, can a bounded wait for it start
+    if (rank == 1 && warp == 1) warp_wait(drain, 0, P.status);
+    __syncwarp();
+    tc::cluster_sync();
+  }
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc_cg<CG>(tmem, G::TMEM_COLS);
+  }
+}
+
+using Narrow = GCfg<1, 64, false>;
+using NarrowF8 = GCfg<1, 64, true>;
+using Wide = GCfg<2, 256, false>;
+using WideF8 = GCfg<2, 256, true>;
+
+template <class G, GroupedMode MODE>
+cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
+  auto kern = grouped_kernel<G, MODE>;
+  static std::atomic<uint64_t> configured{0};  // one attribute call per instantiation and device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e != cudaSuccess) return e;
+    if (G::SPLIT_REGS) {
+      // the split asks for no more registers than the block is launched with, or it would wait forever
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+      if (fa.numRegs * G::THREADS < 128 * (kRegsControl + 2 * kRegsEpilogue)) return cudaErrorInvalidConfiguration;
+    }
+    configured.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(G::THREADS);
+  cfg.dynamicSmemBytes = G::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = G::CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = G::CG == 1 ? 1 : 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return e;
+  count_launches();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int grouped_tile_cols(GroupedKernel k) { return k == GG_WIDE ? Wide::BN : Narrow::BN; }
+int grouped_tile_lanes(GroupedKernel k) { return k == GG_WIDE ? Wide::LANES : Narrow::LANES; }
+
+cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
+                           cudaStream_t stream) {
+  if (fp8) {
+    if (mode != GG_FWD) return cudaErrorInvalidValue;
+    return k == GG_WIDE ? launch_one<WideF8, GG_FWD>(a, grid, stream) : launch_one<NarrowF8, GG_FWD>(a, grid, stream);
+  }
+  switch (mode) {
+    case GG_FWD:
+      return k == GG_WIDE ? launch_one<Wide, GG_FWD>(a, grid, stream) : launch_one<Narrow, GG_FWD>(a, grid, stream);
+    case GG_DX:
+      return k == GG_WIDE ? launch_one<Wide, GG_DX>(a, grid, stream) : launch_one<Narrow, GG_DX>(a, grid, stream);
+    default:
+      return k == GG_WIDE ? launch_one<Wide, GG_DW>(a, grid, stream) : launch_one<Narrow, GG_DW>(a, grid, stream);
+  }
+}
+
+}  // namespace tileq

@@ -1,0 +1,48 @@
+// Arguments and launch entry point of the experts' grouped products (grouped.cu).
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace tileq {
+
+constexpr int kGroupedMaxE = 256;
+
+// What the product reduces over and writes:
+//   GG_FWD  y[p][o]     = sum_i W[e][o][i]  x[p][i]
+//   GG_DX   dx[p][i]    = sum_o W[e][o][i] dy[p][o]
+//   GG_DW   dW[e][o][i] = sum over the rows p of e of dy[p][o] x[p][i]
+enum GroupedMode { GG_FWD = 0, GG_DX = 1, GG_DW = 2 };
+
+struct GroupedArgs {
+  // a: the operand of the output's contiguous dimension (128 TMEM lanes per
+  // CTA), b: that of the output's rows (TMEM columns)
+  alignas(64) CUtensorMap amap;
+  alignas(64) CUtensorMap bmap;
+  const int32_t *offsets;  // device [E + 1], or null: one expert with all P rows
+  int E, P;
+  int L;                   // contiguous output dimension
+  int C;                   // GG_DW: output rows per expert
+  int R;                   // GG_FWD, GG_DX: reduction length
+  int nL;                  // lane tiles
+  int bf16;                // 16-bit operands: 1 bf16, 0 fp16
+  void *out;
+  int out_dtype;           // TILEQ_DT_*
+  int pair_store;          // two neighbouring outputs of 16 bits may be stored as one word
+  long long ldo, out_stride;
+  const float *xs;         // fp8: scales of the rows [R / 128][ld_xs], of the weights [E][nLb][nKb]
+  const float *ws;
+  long long ld_xs;
+  int nLb, nKb;
+  int *status;
+};
+
+enum GroupedKernel { GG_NARROW = 0, GG_WIDE = 1 };
+// Rows of the output (TMEM columns) and lanes per tile of each kernel.
+int grouped_tile_cols(GroupedKernel k);
+int grouped_tile_lanes(GroupedKernel k);
+// fp8 != 0: e4m3 operands with block scales (GG_FWD only).
+cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
+                           cudaStream_t stream);
+
+}  // namespace tileq
