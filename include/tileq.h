@@ -392,6 +392,50 @@ tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const
 tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const void *dy, void *dw, void *ws,
                                    size_t ws_bytes, tileq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The same product with 8-bit operands: e4m3 values (finite ones up to 448, and
+ * NaN) with an fp32 scale for every 128 columns of a row of x and for every
+ * 128 x 128 block of W_e,
+ *   y[p][o] = sum over blocks b of 128 inputs of
+ *             xs[b][p] * ws[e][o / 128][b] * sum over i in b of xq[p][i] * wq[e][o][i]
+ * summed in fp32 and rounded once to out_dtype.  The scales may have any value.
+ * A last block of fewer than 128 inputs or outputs has a scale like the others.
+ *
+ * The quantisers choose scale = the smallest power of two s with max|v| / s <=
+ * 448 over the block's values v, at least 2^-126, and 1 for a block of zeros;
+ * q = v / s (exact) rounded to e4m3, ties to even.  A block with a NaN or an
+ * infinity becomes NaN: its scale and all its values.  Scales, row numbers and
+ * row factors need the alignment of their elements only.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int dtype;              /* x: TILEQ_DT_BF16, TILEQ_DT_F16 or TILEQ_DT_F32 */
+  int R, T, C;            /* rows of q, rows of x, columns of q (>= 1) */
+  int swiglu;             /* 1: x has 2C columns, gate then up, and v = silu(gate) * up in fp32; 0: v = x */
+  const int32_t *rows;    /* device [R]: row r of q comes from row rows[r] of x (the gather of routed tokens; a
+                             number outside [0, T) gives a row of zeros).  NULL: row r, T >= R */
+  const float *row_scale; /* device [R]: v *= row_scale[r] (a routing weight), or NULL */
+  int64_t ld_x, ld_q;     /* row strides in elements, 0 = contiguous, else no less than a row */
+  int64_t ld_s;           /* stride of the scales, 0 = R */
+} tileq_fp8_rows;
+
+/* q device e4m3 [R, C], scales device fp32 [ceil(C / 128), R] (all of a block
+ * before the next).  Asynchronous; R == 0 enqueues nothing. */
+tileq_status tileq_fp8_quantize(const tileq_fp8_rows *a, const void *x, void *q, float *scales,
+                                tileq_stream_t stream);
+
+/* g: dtype (BF16, F16 or F32), E, d_in, d_out, ld_w and stride_w of w; the other
+ * fields are not used.  q device e4m3 [E, d_out, d_in] with strides ld_q and
+ * stride_q (0 = contiguous), scales device fp32 [E, ceil(d_out / 128), ceil(d_in / 128)]. */
+tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, void *q, int64_t ld_q,
+                                        int64_t stride_q, float *scales, tileq_stream_t stream);
+
+/* g: dtype TILEQ_DT_E4M3, out_dtype, sizes, strides (ld_x, ld_w and stride_w
+ * multiples of 16) and offsets as for tileq_grouped_gemm; with expert_offsets
+ * NULL and E = 1 a dense product.  xs device fp32 [ceil(d_in / 128), P], rows
+ * ld_xs apart (0 = P); w_scales device fp32 [E, ceil(d_out / 128), ceil(d_in / 128)]. */
+tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float *xs, int64_t ld_xs, const void *wq,
+                            const float *w_scales, void *y, void *ws, size_t ws_bytes, tileq_stream_t stream);
+
 /* Synchronously read (and clear) the device status word in `ws`.
  * *status receives TILEQ_OK or the first device error recorded. */
 tileq_status tileq_device_status(void *ws, int *status, tileq_stream_t stream);

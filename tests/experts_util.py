@@ -65,3 +65,59 @@ def ref_dw(x, dy, off):
         xe, ye = x[a:b].double(), dy[a:b].double()
         d[e], m[e] = ye.t() @ xe, ye.abs().t() @ xe.abs()
     return d, m
+
+
+# ------------------------------------------------------------------ e4m3 with a scale per block of 128
+def round_e4m3(v):
+    """64-bit values of magnitude <= 448 rounded to e4m3, ties to even: steps 2^(exponent - 3), at least 2^-9."""
+    _, e = torch.frexp(v)
+    step = torch.ldexp(torch.ones_like(v), torch.clamp(e - 4, min=-9))
+    return torch.round(v / step) * step
+
+
+def block_scale(amax):
+    """Smallest power of two s >= 2^-126 with amax / s <= 448 (1 for 0, NaN where amax is not finite), searched."""
+    s = torch.full_like(amax, 2.0 ** -126)
+    for _ in range(260):
+        s = torch.where(amax / s > 448.0, s * 2, s)
+    s = torch.where(amax == 0, torch.ones_like(s), s)
+    return torch.where(torch.isfinite(amax), s, torch.full_like(s, float("nan")))
+
+
+def ref_quant_rows(v):
+    """(values / scale [R, C], scales [ceil(C / 128), R]) of 64-bit rows."""
+    q, sc = torch.empty_like(v), []
+    for c in range(0, v.shape[1], 128):
+        part = v[:, c:c + 128]
+        top = part.abs().amax(1)
+        s = block_scale(torch.where(torch.isnan(part).any(1), torch.full_like(top, float("nan")), top))
+        q[:, c:c + 128] = round_e4m3(part / s[:, None])
+        sc.append(s)
+    return q, torch.stack(sc)
+
+
+def ref_quant_weights(w):
+    E, O, I = w.shape
+    q = torch.empty_like(w)
+    s = torch.empty(E, -(-O // 128), -(-I // 128), dtype=torch.float64, device=w.device)
+    for o in range(0, O, 128):
+        for i in range(0, I, 128):
+            part = w[:, o:o + 128, i:i + 128]
+            s[:, o // 128, i // 128] = sc = block_scale(part.abs().amax((1, 2)))
+            q[:, o:o + 128, i:i + 128] = round_e4m3(part / sc[:, None, None])
+    return q, s
+
+
+def dequant_rows(q, s):
+    return q.float().double() * s.t().double().repeat_interleave(128, 1)[:, :q.shape[1]]
+
+
+def dequant_weights(q, s):
+    s = s.double().repeat_interleave(128, -2).repeat_interleave(128, -1)
+    return q.float().double() * s[..., :q.shape[-2], :q.shape[-1]]
+
+
+def fp8_terms(d_in):
+    """Roundings of an fp8 product, in units of 2^-23 of the magnitudes: the additions of the products, and per
+    block of 128 one rounding of the scales' product and one of the block's addition."""
+    return d_in + 2 * -(-d_in // 128)

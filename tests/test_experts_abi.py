@@ -73,6 +73,79 @@ def test_no_rows_enqueue_nothing(L, name):
     assert _call(L, name, P=0, a=None, out=None) == L.TILEQ_OK
 
 
+# ------------------------------------------------------------------ fp8
+def test_fp8_rows_layout_matches_c(L, tmp_path):
+    names = [f[0] for f in L.tileq_fp8_rows._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "tileq.h"\nint main(void){printf("%zu", sizeof(tileq_fp8_rows));\n'
+                   + "".join(f'printf(" %zu", offsetof(tileq_fp8_rows, {n}));\n' for n in names) + 'return 0;}\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
+    assert got == [ctypes.sizeof(L.tileq_fp8_rows), *(getattr(L.tileq_fp8_rows, n).offset for n in names)]
+
+
+def _fp8(L, xq=A16, xs=A16, ld_xs=0, wq=A16, sw=A16, y=A16, ws=A16, ws_bytes=256, **fields):
+    g = L.tileq_grouped(L.TILEQ_DT_E4M3, 0, 4, 32, 64, 128, 0, 0, 0, 0, A16)
+    for k, v in fields.items():
+        setattr(g, k, v)
+    return L.lib().tileq_fp8_gemm(ctypes.byref(g), xq, xs, ld_xs, wq, sw, y, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(E=0), dict(E=257), dict(P=-1), dict(d_in=0), dict(d_out=0), dict(dtype=0), dict(dtype=4), dict(out_dtype=3),
+    dict(ld_x=-16), dict(ld_x=32), dict(ld_w=32), dict(stride_w=64), dict(expert_offsets=None), dict(xq=None), dict(wq=None),
+    dict(y=None), dict(xs=None), dict(sw=None), dict(xs=A16 + 2), dict(sw=A16 + 2), dict(xq=ODD), dict(wq=ODD), dict(y=ODD),
+    dict(ld_xs=31), dict(ld_xs=-1), dict(ws=None),
+])
+def test_fp8_gemm_invalid(L, bad):
+    assert _fp8(L, **bad) == L.TILEQ_ERR_INVALID_ARG
+
+
+def test_fp8_gemm_refusals(L):
+    assert _fp8(L, ws_bytes=0) == L.TILEQ_ERR_WORKSPACE
+    for bad in (dict(d_in=72), dict(ld_x=72), dict(ld_w=72), dict(stride_w=64 * 128 + 8)):
+        assert _fp8(L, **bad) == L.TILEQ_ERR_UNSUPPORTED
+    assert _fp8(L, P=0, xq=None, xs=None, y=None) == L.TILEQ_OK
+
+
+def _quant(L, x=A16, q=A16, s=A16, **fields):
+    a = L.tileq_fp8_rows(0, 32, 32, 64, 0, None, None, 0, 0, 0)
+    for k, v in fields.items():
+        setattr(a, k, v)
+    return L.lib().tileq_fp8_quantize(ctypes.byref(a), x, q, s, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=3), dict(dtype=-1), dict(R=-1), dict(T=-1), dict(C=0), dict(swiglu=2), dict(T=31), dict(ld_x=63), dict(ld_x=-1),
+    dict(ld_q=63), dict(ld_s=31), dict(swiglu=1, ld_x=127), dict(rows=A16 + 2), dict(row_scale=A16 + 1), dict(x=None),
+    dict(q=None), dict(s=None), dict(x=ODD), dict(q=ODD), dict(s=A16 + 2),
+])
+def test_fp8_quantize_invalid(L, bad):
+    assert _quant(L, **bad) == L.TILEQ_ERR_INVALID_ARG
+
+
+def test_fp8_quantize_no_rows(L):
+    assert _quant(L, R=0, x=None, q=None, s=None) == L.TILEQ_OK
+    assert L.lib().tileq_fp8_quantize(None, A16, A16, A16, None) == L.TILEQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=3), dict(E=0), dict(E=257), dict(d_in=0), dict(d_out=0), dict(ld_w=63), dict(stride_w=64 * 127), dict(w=None),
+    dict(q=None), dict(s=None), dict(w=ODD), dict(q=ODD), dict(ld_q=63), dict(ld_q=-1), dict(stride_q=64), dict(s=A16 + 2),
+])
+def test_fp8_quantize_weights_invalid(L, bad):
+    g = L.tileq_grouped(0, 0, 4, 0, 64, 128, 0, 0, 0, 0, None)
+    a = dict(w=A16, q=A16, ld_q=0, stride_q=0, s=A16)
+    for k, v in bad.items():
+        if k in a:
+            a[k] = v
+        else:
+            setattr(g, k, v)
+    assert L.lib().tileq_fp8_quantize_weights(ctypes.byref(g), a["w"], a["q"], a["ld_q"], a["stride_q"], a["s"],
+                                              None) == L.TILEQ_ERR_INVALID_ARG
+
+
 def test_tensors_that_do_not_fit():
     torch = pytest.importorskip("torch")
     import tiled_rank_b200 as tq
@@ -85,6 +158,12 @@ def test_tensors_that_do_not_fit():
         tq.grouped_gemm_dx(torch.zeros(8, 16).half(), w.half(), off)
     with pytest.raises(ValueError):
         tq.grouped_gemm_dw(x.bfloat16(), torch.zeros(8, 16).bfloat16(), off)
+    with pytest.raises(ValueError):
+        tq.fp8_quantize(x.bfloat16())
+    with pytest.raises(ValueError):
+        tq.fp8_quantize_weights(w.bfloat16())
+    with pytest.raises(ValueError):
+        tq.fp8_gemm(x, x, w, w, off)
     with pytest.raises(AttributeError):
         tq.no_such_product
     assert "grouped_gemm" in dir(tq)

@@ -14,12 +14,14 @@ from ._lib import (  # noqa: F401
     tileq_wbig, tileq_sketch_workspace_size, tileq_sketch_lowrank,
     tileq_place_in, tileq_place_out, place_in, tileq_place_workspace_size, tileq_place_experts,
     TILEQ_DT_BF16, TILEQ_DT_F16, TILEQ_DT_F32, TILEQ_DT_E4M3, tileq_grouped,
-    tileq_grouped_gemm, tileq_grouped_gemm_dx, tileq_grouped_gemm_dw,
+    tileq_grouped_gemm, tileq_grouped_gemm_dx, tileq_grouped_gemm_dw, tileq_fp8_rows,
+    tileq_fp8_quantize, tileq_fp8_quantize_weights, tileq_fp8_gemm,
 )
 from .layer import DeviceLayer  # noqa: F401
 
 # the products with the experts' uncompressed weights work on torch tensors: torch is imported with their first use
-_EXPERTS = ("expert_status", "grouped_gemm", "grouped_gemm_dw", "grouped_gemm_dx")
+_EXPERTS = ("expert_status", "fp8_gemm", "fp8_quantize", "fp8_quantize_weights", "grouped_gemm",
+            "grouped_gemm_dw", "grouped_gemm_dx")
 
 
 def __getattr__(name):

@@ -41,6 +41,7 @@ EXPORTS = (
     "tileq_sketch_workspace_size", "tileq_sketch_lowrank",
     "tileq_place_workspace_size", "tileq_place_experts",
     "tileq_grouped_gemm", "tileq_grouped_gemm_dx", "tileq_grouped_gemm_dw",
+    "tileq_fp8_quantize", "tileq_fp8_quantize_weights", "tileq_fp8_gemm",
 )
 TILEQ_SKETCH_MAX_L = 160
 TILEQ_PLACE_MAX_R0 = 256
@@ -113,11 +114,19 @@ class tileq_grouped(ctypes.Structure):
     ]
 
 
+class tileq_fp8_rows(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("R", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
+        ("swiglu", ctypes.c_int), ("rows", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64), ("ld_q", ctypes.c_int64), ("ld_s", ctypes.c_int64),
+    ]
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with `python -m tiled_rank_b200.build`")
     lib = ctypes.CDLL(path)
-    c_int, c_size, vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    c_int, c_size, vp, c_i64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
     P = ctypes.POINTER
     sigs = {
         "tileq_status_string": ([c_int], ctypes.c_char_p),
@@ -143,6 +152,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tileq_grouped_gemm": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
         "tileq_grouped_gemm_dx": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
         "tileq_grouped_gemm_dw": ([P(tileq_grouped), vp, vp, vp, vp, c_size, vp], c_int),
+        "tileq_fp8_quantize": ([P(tileq_fp8_rows), vp, vp, vp, vp], c_int),
+        "tileq_fp8_quantize_weights": ([P(tileq_grouped), vp, vp, c_i64, c_i64, vp, vp], c_int),
+        "tileq_fp8_gemm": ([P(tileq_grouped), vp, vp, c_i64, vp, vp, vp, vp, c_size, vp], c_int),
     }
     for name, (argtypes, restype) in sigs.items():
         fn = getattr(lib, name)
@@ -337,3 +349,19 @@ def tileq_grouped_gemm_dx(g: tileq_grouped, dy, w, dx, ws, stream=None):
 
 def tileq_grouped_gemm_dw(g: tileq_grouped, x, dy, dw, ws, stream=None):
     _grouped("tileq_grouped_gemm_dw", g, x, dy, dw, ws, stream)
+
+
+def tileq_fp8_quantize(a: tileq_fp8_rows, x, q, scales, stream=None):
+    _check(lib().tileq_fp8_quantize(ctypes.byref(a), _ptr(x), _ptr(q), _ptr(scales), _stream(stream)),
+           "tileq_fp8_quantize")
+
+
+def tileq_fp8_quantize_weights(g: tileq_grouped, w, q, ld_q: int, stride_q: int, scales, stream=None):
+    _check(lib().tileq_fp8_quantize_weights(ctypes.byref(g), _ptr(w), _ptr(q), ld_q, stride_q, _ptr(scales),
+                                            _stream(stream)), "tileq_fp8_quantize_weights")
+
+
+def tileq_fp8_gemm(g: tileq_grouped, xq, xs, ld_xs: int, wq, w_scales, y, ws, stream=None):
+    _check(lib().tileq_fp8_gemm(ctypes.byref(g), _ptr(xq), _ptr(xs), ld_xs, _ptr(wq), _ptr(w_scales), _ptr(y), _ptr(ws),
+                                ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)),
+           "tileq_fp8_gemm")

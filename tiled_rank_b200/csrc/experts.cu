@@ -1,16 +1,18 @@
 // C ABI of the experts' products (include/tileq.h): argument checks, tensor maps
-// and the choice of kernel.  The kernels are in grouped.cu.
+// and the choice of kernel.  The kernels are in grouped.cu and fp8.cu.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstring>
 
+#include "fp8.cuh"
 #include "grouped.cuh"
 #include "kernels.cuh"
 
 namespace tileq {
 namespace {
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
 long long div_up(long long v, long long m) { return (v + m - 1) / m; }
@@ -89,7 +91,7 @@ tileq_status check(const tileq_grouped *g, const void *a, const void *b, const v
     return TILEQ_ERR_INVALID_ARG;
   if (g->ld_x < 0 || g->ld_y < 0 || g->ld_w < 0 || g->stride_w < 0) return TILEQ_ERR_INVALID_ARG;
   if (!g->expert_offsets && g->E != 1) return TILEQ_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(g->expert_offsets) & 3) return TILEQ_ERR_INVALID_ARG;
+  if (!aligned4(g->expert_offsets)) return TILEQ_ERR_INVALID_ARG;
   if (!a || !b || !out || !aligned16(a) || !aligned16(b) || !aligned16(out)) return TILEQ_ERR_INVALID_ARG;
   if (!ws) return TILEQ_ERR_INVALID_ARG;
   if (ws_bytes < TILEQ_GROUPED_WS_BYTES) return TILEQ_ERR_WORKSPACE;
@@ -191,6 +193,97 @@ tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const 
   a.status = static_cast<int *>(ws);
   return run(a, GG_DW, g, {x, g->dtype, g->d_in, g->P, 0, s.x, 0}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0}, false,
              reinterpret_cast<cudaStream_t>(stream));
+}
+
+tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float *xs, int64_t ld_xs, const void *wq,
+                            const float *w_scales, void *y, void *ws, size_t ws_bytes, tileq_stream_t stream) {
+  const bool none = g && g->P == 0;
+  tileq_status st = check(g, none ? wq : xq, wq, none ? wq : y, ws, ws_bytes, true);
+  if (st != TILEQ_OK) return st;
+  if ((!xs && !none) || !w_scales || !aligned4(xs) || !aligned4(w_scales) || ld_xs < 0 || (ld_xs && ld_xs < g->P))
+    return TILEQ_ERR_INVALID_ARG;
+  Strides s;
+  if ((st = strides_of(g, 1, false, &s)) != TILEQ_OK) return st;
+  if (s.x % 16 || s.w % 16 || s.we % 16) return TILEQ_ERR_UNSUPPORTED;
+  if (g->P == 0) return TILEQ_OK;
+  GroupedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.L = g->d_out;
+  a.R = g->d_in;
+  a.out = y;
+  a.ldo = s.y;
+  a.xs = xs;
+  a.ws = w_scales;
+  a.ld_xs = ld_xs ? ld_xs : g->P;
+  a.nLb = (int)div_up(g->d_out, 128);
+  a.nKb = (int)div_up(g->d_in, 128);
+  a.status = static_cast<int *>(ws);
+  return run(a, GG_FWD, g, {wq, TILEQ_DT_E4M3, g->d_in, g->d_out, g->E, s.w, s.we},
+             {xq, TILEQ_DT_E4M3, g->d_in, g->P, 0, s.x, 0}, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q, float *scales,
+                                tileq_stream_t stream) {
+  if (!p || p->R < 0 || p->T < 0 || p->C < 1 || p->C > (1 << 26) || (p->swiglu & ~1)) return TILEQ_ERR_INVALID_ARG;
+  if (p->dtype != TILEQ_DT_BF16 && p->dtype != TILEQ_DT_F16 && p->dtype != TILEQ_DT_F32) return TILEQ_ERR_INVALID_ARG;
+  if (p->ld_x < 0 || p->ld_q < 0 || p->ld_s < 0 || (!p->rows && p->T < p->R)) return TILEQ_ERR_INVALID_ARG;
+  if (!aligned4(p->rows) || !aligned4(p->row_scale)) return TILEQ_ERR_INVALID_ARG;
+  const long long width = (long long)p->C * (p->swiglu ? 2 : 1);
+  const long long ld_x = p->ld_x ? p->ld_x : width, ld_q = p->ld_q ? p->ld_q : p->C, ld_s = p->ld_s ? p->ld_s : p->R;
+  if ((p->T > 1 && ld_x < width) || (p->R > 1 && ld_q < p->C) || ld_s < p->R) return TILEQ_ERR_INVALID_ARG;
+  if (p->R == 0) return TILEQ_OK;
+  if (!q || !scales || !aligned16(q) || !aligned4(scales) || (!x && p->T > 0) || !aligned16(x)) return TILEQ_ERR_INVALID_ARG;
+  if (div_up(p->C, 1024) > 65535) return TILEQ_ERR_UNSUPPORTED;
+  const int es = p->dtype == TILEQ_DT_F32 ? 4 : 2;
+  QuantRowsArgs a;
+  a.x = x;
+  a.rows = p->rows;
+  a.row_scale = p->row_scale;
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = scales;
+  a.ld_x = ld_x;
+  a.ld_q = ld_q;
+  a.ld_s = ld_s;
+  a.R = p->R;
+  a.T = p->T;
+  a.C = p->C;
+  a.dtype = p->dtype;
+  a.swiglu = p->swiglu;
+  a.vec_x = (p->T <= 1 || ld_x * es % 16 == 0) && (!p->swiglu || (long long)p->C * es % 16 == 0);
+  a.vec_q = p->R <= 1 || ld_q % 8 == 0;
+  return launch_quant_rows(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILEQ_OK : TILEQ_ERR_CUDA;
+}
+
+tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, void *q, int64_t ld_q,
+                                        int64_t stride_q, float *scales, tileq_stream_t stream) {
+  if (!g || g->E < 1 || g->E > TILEQ_GROUPED_MAX_E || g->d_in < 1 || g->d_out < 1) return TILEQ_ERR_INVALID_ARG;
+  if (g->dtype != TILEQ_DT_BF16 && g->dtype != TILEQ_DT_F16 && g->dtype != TILEQ_DT_F32) return TILEQ_ERR_INVALID_ARG;
+  if (g->ld_w < 0 || g->stride_w < 0 || ld_q < 0 || stride_q < 0) return TILEQ_ERR_INVALID_ARG;
+  QuantWeightsArgs a;
+  a.ld_w = g->ld_w ? g->ld_w : g->d_in;
+  a.ld_q = ld_q ? ld_q : g->d_in;
+  a.stride_w = g->stride_w ? g->stride_w : a.ld_w * g->d_out;
+  a.stride_q = stride_q ? stride_q : a.ld_q * g->d_out;
+  const auto short_of = [&](long long ld, long long stride) {
+    return ld < g->d_in || (g->E > 1 && stride < (long long)(g->d_out - 1) * ld + g->d_in);
+  };
+  if (short_of(a.ld_w, a.stride_w) || short_of(a.ld_q, a.stride_q)) return TILEQ_ERR_INVALID_ARG;
+  if (!w || !q || !scales || !aligned16(w) || !aligned16(q) || !aligned4(scales)) return TILEQ_ERR_INVALID_ARG;
+  const int es = g->dtype == TILEQ_DT_F32 ? 4 : 2;
+  a.w = w;
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = scales;
+  a.d_out = g->d_out;
+  a.d_in = g->d_in;
+  a.nO = (int)div_up(g->d_out, 128);
+  a.nI = (int)div_up(g->d_in, 128);
+  a.dtype = g->dtype;
+  a.vec_w = a.ld_w * es % 16 == 0 && (g->E == 1 || a.stride_w * es % 16 == 0);
+  a.vec_q = a.ld_q % 8 == 0 && (g->E == 1 || a.stride_q % 8 == 0);
+  const long long blocks = (long long)g->E * a.nO * a.nI;
+  if (blocks > 0x7fffffff) return TILEQ_ERR_UNSUPPORTED;
+  return launch_quant_weights(a, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILEQ_OK
+                                                                                                    : TILEQ_ERR_CUDA;
 }
 
 }  // extern "C"
