@@ -42,13 +42,13 @@ bool encode(CUtensorMap *m, const Operand &o, int box_rows) {
   if (!fn) return false;
   const int es = o.dtype == TILEQ_DT_E4M3 ? 1 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)std::max(o.rows, 1ll), (cuuint64_t)std::max(o.mats, 1ll)};
-  const cuuint64_t strides[2] = {(cuuint64_t)(o.ld * es), (cuuint64_t)(o.stride * es)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(o.ld * es), (cuuint64_t)((o.mats ? o.stride : o.ld) * es)};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = o.dtype == TILEQ_DT_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : o.dtype == TILEQ_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  return fn(m, type, o.mats ? 3 : 2, const_cast<void *>(o.base), dims, strides, box, estr,
+  return fn(m, type, 3, const_cast<void *>(o.base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

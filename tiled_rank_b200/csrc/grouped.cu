@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     for (int w = unit0; ok && tiles.get(w, t); w += units) {
       const int nk = steps(t), half = mma_n(t) / CG;
       const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
-      constexpr int BBOX = MODE == GG_DW ? 64 : kBoxRows;  // columns of one box of B
+      constexpr int ABOX = MODE == GG_FWD ? 1 : 2;         // boxes of A: 128 rows, or twice 64 columns
+      constexpr int BBOX = MODE == GG_DW ? 64 : kBoxRows;  // columns of the tile in one box of B
       const int nbox = (half + BBOX - 1) / BBOX;
       const uint32_t bytes = G::A_BYTES + nbox * BBOX * 128;
       for (int kb = 0; kb < nk; ++kb, ++qi) {
@@ -241,33 +242,29 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         const int left = MODE == GG_DW ? t.rows - kb * G::KE : G::KE;
         const bool cut = left < G::KE && (left & 15);  // the last MMA of the step reaches the next expert's rows
         if (qi >= (uint32_t)SQ && !(ok = warp_wait(&empty[s], ((qi / SQ) - 1) & 1, P.status))) break;
+        uint32_t bar = cut ? smem_addr(tail) : CG == 2 ? tc::map_cta(&full[s], 0) : smem_addr(&full[s]);
         if (lane == 0) {
-          uint32_t bar = smem_addr(&full[s]);
-          if (cut) {
-            bar = smem_addr(tail);
-            mbar_arrive_expect_tx(tail, bytes);
-          } else if (CG == 2) {
-            bar = tc::map_cta(&full[s], 0);
+          if (cut || CG == 1)
+            mbar_arrive_expect_tx(cut ? tail : &full[s], bytes);
+          else
             tc::arrive_expect_at(bar, bytes);
+        }
+        // one lane per box: a single lane would need the time of a whole stage to issue five or six copies
+        if (lane < ABOX + nbox) {
+          const bool is_a = lane < ABOX;
+          const int i = is_a ? lane : lane - ABOX;
+          uint8_t *dst = is_a ? stage_a(s) + i * 8192 : stage_b(s) + i * BBOX * 128;
+          const CUtensorMap *map = is_a ? &P.amap : &P.bmap;
+          int x, y, z = 0;
+          if (MODE == GG_FWD || (MODE == GG_DX && !is_a)) {
+            x = kb * G::KE;
+            y = is_a ? l0 : t.row0 + c0 + i * BBOX;
           } else {
-            mbar_arrive_expect_tx(&full[s], bytes);
+            x = (is_a ? l0 : c0) + i * 64;
+            y = (MODE == GG_DW ? t.row0 : 0) + kb * 64;
           }
-          uint8_t *a = stage_a(s), *b = stage_b(s);
-          if constexpr (MODE == GG_FWD) {
-            tc::tma_3d<CG>(a, &P.amap, kb * G::KE, l0, t.e, bar);
-          } else if constexpr (MODE == GG_DX) {
-            tc::tma_3d<CG>(a, &P.amap, l0, kb * 64, t.e, bar);
-            tc::tma_3d<CG>(a + 8192, &P.amap, l0 + 64, kb * 64, t.e, bar);
-          } else {
-            tc::tma_2d<CG>(a, &P.amap, l0, t.row0 + kb * 64, bar);
-            tc::tma_2d<CG>(a + 8192, &P.amap, l0 + 64, t.row0 + kb * 64, bar);
-          }
-          for (int i = 0; i < nbox; ++i) {
-            if constexpr (MODE == GG_DW)
-              tc::tma_2d<CG>(b + i * 8192, &P.bmap, c0 + i * 64, t.row0 + kb * 64, bar);
-            else
-              tc::tma_2d<CG>(b + i * kBoxRows * 128, &P.bmap, kb * G::KE, t.row0 + c0 + i * kBoxRows, bar);
-          }
+          if (is_a && MODE != GG_DW) z = t.e;
+          tc::tma_3d<CG>(dst, map, x, y, z, bar);
         }
         if (cut) {
           __syncwarp();
@@ -373,7 +370,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         if (nk > 0) {
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::arrive_at(tc::map_cta(&acc_empty[ab], 0));
+          if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[ab], 0));
           ++ai;
         }
       } else {
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           }
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::arrive_at(tc::map_cta(&acc_empty[ab], 0));
+          if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[ab], 0));
         }
 #pragma unroll
         for (int ch = 0; ch < G::COLS / 16; ++ch) {

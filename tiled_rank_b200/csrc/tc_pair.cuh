@@ -94,10 +94,16 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
+// The arrival publishes nothing of this thread's (the copies it announces report themselves): relaxed, since a
+// release at cluster scope makes the thread wait for its earlier accesses, a microsecond in a producer's loop.
 __device__ __forceinline__ void arrive_expect_at(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_addr),
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
+}
+// An arrival that orders tensor-memory reads only (after wait::ld and tcgen05.fence::before_thread_sync).
+__device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
 // mbar_wait with cluster-scope acquire: the arrivals may come from another CTA.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -126,21 +132,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
 // Tile loads whose completion is counted on the mbarrier at cluster address
 // `bar` (CG == 2: this CTA's or the pair's first CTA's).  No multicast: every
 // CTA loads its own tiles into its own shared memory.
-template <int CG>
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];\n" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3}], [%4];\n" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
 template <int CG>
 __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   if constexpr (CG == 1)
