@@ -358,9 +358,9 @@ tileq_status tileq_place_experts(const tileq_place_in *in, tileq_place_out *out,
  * bits on every run.
  *
  * The offsets are read on the device, so a call can be captured into a graph
- * and replayed with other routings.  Offsets outside [0, P] are cut to it and a
- * falling pair counts as no rows, so no value of theirs leads out of the arrays;
- * ranges that overlap give unspecified rows.
+ * and replayed with other routings.  Offsets outside [0, P] are cut to it and one
+ * below its predecessor counts as equal to it, so no value of theirs leads out of
+ * the arrays.
  *
  * ws: device workspace of at least TILEQ_GROUPED_WS_BYTES, zeroed once by the
  * caller.  It holds the status word alone (tileq_device_status), which bounded

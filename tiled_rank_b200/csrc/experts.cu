@@ -120,7 +120,7 @@ tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const
   a.pair_store = g->out_dtype != TILEQ_DT_F32 && a.L % 2 == 0 && a.ldo % 2 == 0 && a.out_stride % 2 == 0;
   const long long tiles = a.nL * (mode == GG_DW ? (long long)g->E * div_up(a.C, bn) : g->P / bn + std::min(g->E, g->P));
   if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
-  if (!encode(&a.amap, oa, mode == GG_FWD ? 128 : 64) || !encode(&a.bmap, ob, mode == GG_DW ? 64 : 32))
+  if (!encode(&a.amap, oa, mode == GG_FWD ? 128 : 64) || !encode(&a.bmap, ob, mode == GG_DW ? 64 : grouped_box_rows(k)))
     return TILEQ_ERR_CUDA;
   const int sms = sm_count();
   if (sms < cg) return TILEQ_ERR_CUDA;

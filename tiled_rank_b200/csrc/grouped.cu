@@ -20,11 +20,12 @@
 // half of B's, so an SM reads 32 KB per 64-element step of a 256 x 256 tile
 // instead of 48 KB).  Warps of a CTA:
 //   0      producer: TMA tiles (128-byte swizzle) of one 128-byte reduction step
-//          per stage into a ring; in GG_DW it also zeroes the rows of the next
-//          expert in the last step (both operands: 0 * NaN would be NaN);
+//          per stage into a ring;
 //   1      MMA issuer (first CTA of a pair): four MMAs per stage into an fp32
 //          TMEM accumulator, two or four accumulators in turn;
 //   2      the table of the experts' rows and tiles, before the others start;
+//   3      in GG_DW zeroes the rows of the next expert in the last stage of a
+//          tile (of both operands: 0 * NaN would be NaN);
 //   4..    epilogue: TMEM to registers, one rounding, stores.
 // fp8: one 128-byte stage is one scale block.  Every block gets an accumulator
 // of its own, which the epilogue warps fold into fp32 registers with
@@ -41,7 +42,6 @@
 namespace tileq {
 namespace {
 
-constexpr int kBoxRows = 32;        // rows of one box of a row operand (B of GG_FWD, GG_DX)
 constexpr int kFirstEpw = 4;        // first epilogue warp
 constexpr int kRegsControl = 56, kRegsEpilogue = 224;  // registers a thread where the warps split them
 constexpr int kRowTileGroup = 8;    // column tiles that share a pass over the lane tiles
@@ -52,6 +52,7 @@ struct GCfg {
   static constexpr bool F8 = F8_;
   static constexpr int LANES = 128 * CG;
   static constexpr int KE = F8 ? 128 : 64;  // reduction elements per stage (128 bytes)
+  static constexpr int BOX_ROWS = BN == 256 ? 64 : 32;  // rows of one box of a row operand (B of GG_FWD, GG_DX)
   static constexpr int EPW = BN == 256 ? 8 : 4;
   static constexpr int COLS = BN / (EPW / 4);  // columns of one epilogue warp
   static constexpr int THREADS = (kFirstEpw + EPW) * 32;
@@ -59,13 +60,14 @@ struct GCfg {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = BN / CG * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int SQ = 200 * 1024 / STAGE;
+  static constexpr int TAB = (2 * kGroupedMaxE + 2) * 4;
+  static constexpr int SQ = (227 * 1024 - TAB - (F8 ? 2 * BN * 4 : 0) - 512) / STAGE;
   static constexpr int NACC = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = NACC * BN;
   static constexpr int BAR_OFF = SQ * STAGE;
-  static constexpr int SCALE_OFF = BAR_OFF + (2 * SQ + 2 * NACC + 2) * 8 + 16;
+  static constexpr int SCALE_OFF = BAR_OFF + ((3 * SQ + 2 * NACC + 1) * 8 + 31) / 16 * 16;
   static constexpr int TAB_OFF = SCALE_OFF + (F8 ? 2 * BN * 4 : 0);
-  static constexpr int SMEM = TAB_OFF + (3 * kGroupedMaxE + 1) * 4 + 1024;
+  static constexpr int SMEM = TAB_OFF + TAB;
   static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two of tensor memory columns");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -80,12 +82,12 @@ struct Tile {
 // tiles, so that the CTAs at work read few distinct rows of either operand.
 template <class G, GroupedMode MODE>
 struct Tiles {
-  const int *first, *beg, *cnt;
+  const int *first, *beg;
   int E, L, nL, C, e = 0;
   __device__ bool get(int w, Tile &t) {
     if (w >= first[E]) return false;
     while (w >= first[e + 1]) ++e;
-    const int i = w - first[e], total = MODE == GG_DW ? C : cnt[e];
+    const int i = w - first[e], rows = beg[e + 1] - beg[e], total = MODE == GG_DW ? C : rows;
     const int nc = (total + G::BN - 1) / G::BN;
     const int grp = i / (kRowTileGroup * nL), rem = i - grp * kRowTileGroup * nL;
     const int gsz = min(kRowTileGroup, nc - grp * kRowTileGroup);
@@ -94,7 +96,7 @@ struct Tiles {
     const int step = 16 * G::CG, tc = ((total + nc - 1) / nc + step - 1) / step * step;
     t.e = e;
     t.row0 = beg[e];
-    t.rows = cnt[e];
+    t.rows = rows;
     t.l0 = l * G::LANES;
     t.c0 = c * tc;
     t.ncols = min(tc, total - t.c0);
@@ -112,59 +114,80 @@ __device__ __forceinline__ void wait16(uint32_t (&r)[16]) {
 }
 
 // mbar_wait by a whole warp with one answer: no lane leaves a loop in which the others still meet.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status) {
-  return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, status));
+// (`remote`: the pair's other CTA has written memory before it arrived.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status, bool remote = false) {
+  return __all_sync(0xffffffffu, remote ? tc::mbar_wait_cluster(bar, parity, status) : mbar_wait(bar, parity, status));
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype) {
-  if (dtype == TILEQ_DT_BF16) {
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == TILEQ_DT_BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    return h2_as_u32(__floats2half2_rn(lo, hi));
   }
-  return h2_as_u32(__floats2half2_rn(lo, hi));
 }
 
-// Columns c .. c + 15 of this warp's 32 lanes (l: this thread's) to out + column * ldo + l.
-__device__ __forceinline__ void store16(const GroupedArgs &P, long long base, int c, int ncols, int l, int lane,
-                                        const float (&v)[16]) {
-  if (P.out_dtype == TILEQ_DT_F32) {
-    float *out = reinterpret_cast<float *>(P.out) + base + l;
+// Columns c .. c + 15 of this warp's 32 lanes, 16-bit results: lanes 2j and 2j + 1
+// exchange so that each stores two neighbouring outputs of one column (PAIR), else one by one.
+template <int DT, bool PAIR>
+__device__ __forceinline__ void store16_b16(uint16_t *out, long long ldo, int n, bool in, int odd, const float (&v)[16]) {
+  if constexpr (PAIR) {
+    out += odd ? ldo - 1 : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < ncols && l < P.L) out[(long long)(c + i) * P.ldo] = v[i];
-  } else if (P.pair_store) {
-    // lanes 2j and 2j + 1 exchange so that each stores two neighbouring outputs of one column
-    const int odd = lane & 1;
-    uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base + (l & ~1);
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
+    for (int i = 0; i < 16; i += 2, out += 2 * ldo) {
       const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-      const uint32_t w = odd ? pack2(got, v[i + 1], P.out_dtype) : pack2(v[i], got, P.out_dtype);
-      if (c + i + odd < ncols && l < P.L)
-        *reinterpret_cast<uint32_t *>(out + (long long)(c + i + odd) * P.ldo) = w;
+      const uint32_t w = pack2<DT>(odd ? got : v[i], odd ? v[i + 1] : got);
+      if (in && i + odd < n) *reinterpret_cast<uint32_t *>(out) = w;
     }
   } else {
-    uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base + l;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < ncols && l < P.L) out[(long long)(c + i) * P.ldo] = (uint16_t)pack2(v[i], 0.f, P.out_dtype);
+    for (int i = 0; i < 16; ++i, out += ldo)
+      if (in && i < n) *out = (uint16_t)pack2<DT>(v[i], 0.f);
+  }
+}
+
+// Columns c .. c + 15 of this warp's 32 lanes (l: this thread's) to out + base + column * ldo + l.
+__device__ __forceinline__ void store16(const GroupedArgs &P, long long base, int c, int ncols, int l, int lane,
+                                        const float (&v)[16]) {
+  const bool in = l < P.L;
+  const int n = ncols - c, odd = lane & 1;
+  base += c * P.ldo + l;
+  if (P.out_dtype == TILEQ_DT_F32) {
+    float *out = reinterpret_cast<float *>(P.out) + base;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, out += P.ldo)
+      if (in && i < n) *out = v[i];
+    return;
+  }
+  uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base;
+  if (P.out_dtype == TILEQ_DT_BF16) {
+    if (P.pair_store)
+      store16_b16<TILEQ_DT_BF16, true>(out, P.ldo, n, in, odd, v);
+    else
+      store16_b16<TILEQ_DT_BF16, false>(out, P.ldo, n, in, odd, v);
+  } else {
+    if (P.pair_store)
+      store16_b16<TILEQ_DT_F16, true>(out, P.ldo, n, in, odd, v);
+    else
+      store16_b16<TILEQ_DT_F16, false>(out, P.ldo, n, in, odd, v);
   }
 }
 
 template <class G, GroupedMode MODE>
 __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_constant__ GroupedArgs P) {
   constexpr int CG = G::CG, SQ = G::SQ, NACC = G::NACC;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle wants tiles at multiples of 1024
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF);
   uint64_t *empty = full + SQ;
   uint64_t *acc_full = empty + SQ;
   uint64_t *acc_empty = acc_full + NACC;
-  uint64_t *tail = acc_empty + NACC;  // GG_DW: the copies of a step with foreign rows
-  uint64_t *drain = tail + 1;
+  uint64_t *tail = acc_empty + NACC;  // [SQ] GG_DW: the copies of a stage with foreign rows
+  uint64_t *drain = tail + SQ;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   float *scale = reinterpret_cast<float *>(smem + G::SCALE_OFF);
-  int *first = reinterpret_cast<int *>(smem + G::TAB_OFF), *beg = first + kGroupedMaxE + 1, *cnt = beg + kGroupedMaxE;
+  int *first = reinterpret_cast<int *>(smem + G::TAB_OFF), *beg = first + kGroupedMaxE + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : tc::cluster_rank();
@@ -176,12 +199,12 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     for (int s = 0; s < SQ; ++s) {
       mbar_init(&full[s], CG);
       mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
     }
     for (int b = 0; b < NACC; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], G::EPW * CG);
     }
-    mbar_init(tail, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -189,25 +212,27 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   // the prologue overlaps the previous kernel's tail
   pdl_wait_and_release();
   if (warp == 2) {
-    // rows and tiles of each expert; offsets outside [0, P] or falling ones are cut to what is in range
-    int before = 0;
+    // rows and tiles of each expert; offsets outside [0, P] are cut to it, one below its predecessor is raised to it
+    int before = 0, top = P.offsets ? min(max(P.offsets[0], 0), P.P) : 0;
+    if (lane == 0) beg[0] = top;
     for (int e0 = 0; e0 < P.E; e0 += 32) {
       const int e = e0 + lane;
-      int n = 0;
-      if (e < P.E) {
-        const int lo = P.offsets ? min(max(P.offsets[e], 0), P.P) : 0;
-        const int hi = P.offsets ? min(max(P.offsets[e + 1], lo), P.P) : P.P;
-        beg[e] = lo;
-        cnt[e] = hi - lo;
-        n = P.nL * (((MODE == GG_DW ? P.C : hi - lo) + G::BN - 1) / G::BN);
+      int hi = top;
+      if (e < P.E) hi = P.offsets ? min(max(P.offsets[e + 1], top), P.P) : P.P;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, hi, d);
+        if (lane >= d) hi = max(hi, o);
       }
-      int sum = n;
+      int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+      if (lane == 0) lo = top;
+      int sum = e < P.E ? P.nL * (((MODE == GG_DW ? P.C : hi - lo) + G::BN - 1) / G::BN) : 0;
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
       }
-      if (e < P.E) first[e + 1] = before + sum;
+      if (e < P.E) beg[e + 1] = hi, first[e + 1] = before + sum;
       before += __shfl_sync(0xffffffffu, sum, 31);
+      top = __shfl_sync(0xffffffffu, hi, 31);
     }
     if (lane == 0) first[0] = 0;
   }
@@ -217,7 +242,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Tiles<G, MODE> tiles{first, beg, cnt, P.E, P.L, P.nL, P.C};
+  Tiles<G, MODE> tiles{first, beg, P.E, P.L, P.nL, P.C};
   auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
   // columns of the tile's MMA
   auto mma_n = [&](const Tile &t) { return (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG); };
@@ -229,12 +254,12 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   }
   if (warp == 0) {
     // ============================================================ producer
-    uint32_t qi = 0, tails = 0;
+    uint32_t qi = 0;
     for (int w = unit0; ok && tiles.get(w, t); w += units) {
       const int nk = steps(t), half = mma_n(t) / CG;
       const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
       constexpr int ABOX = MODE == GG_FWD ? 1 : 2;         // boxes of A: 128 rows, or twice 64 columns
-      constexpr int BBOX = MODE == GG_DW ? 64 : kBoxRows;  // columns of the tile in one box of B
+      constexpr int BBOX = MODE == GG_DW ? 64 : G::BOX_ROWS;  // columns of the tile in one box of B
       const int nbox = (half + BBOX - 1) / BBOX;
       const uint32_t bytes = G::A_BYTES + nbox * BBOX * 128;
       for (int kb = 0; kb < nk; ++kb, ++qi) {
@@ -242,10 +267,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         const int left = MODE == GG_DW ? t.rows - kb * G::KE : G::KE;
         const bool cut = left < G::KE && (left & 15);  // the last MMA of the step reaches the next expert's rows
         if (qi >= (uint32_t)SQ && !(ok = warp_wait(&empty[s], ((qi / SQ) - 1) & 1, P.status))) break;
-        uint32_t bar = cut ? smem_addr(tail) : CG == 2 ? tc::map_cta(&full[s], 0) : smem_addr(&full[s]);
+        const uint32_t bar = cut ? smem_addr(&tail[s]) : CG == 2 ? tc::map_cta(&full[s], 0) : smem_addr(&full[s]);
         if (lane == 0) {
           if (cut || CG == 1)
-            mbar_arrive_expect_tx(cut ? tail : &full[s], bytes);
+            mbar_arrive_expect_tx(cut ? &tail[s] : &full[s], bytes);
           else
             tc::arrive_expect_at(bar, bytes);
         }
@@ -265,20 +290,6 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           }
           if (is_a && MODE != GG_DW) z = t.e;
           tc::tma_3d<CG>(dst, map, x, y, z, bar);
-        }
-        if (cut) {
-          __syncwarp();
-          if (!(ok = warp_wait(tail, tails++ & 1, P.status))) break;
-          const int to = (left + 15) & ~15;
-          for (int i = lane; i < (to - left) * 8; i += 32) {
-            const int off = (left + i / 8) * 128 + (i % 8) * 16;  // whole rows: the swizzle stays inside a row
-            for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4 *>(stage_a(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
-            for (int j = 0; j < nbox; ++j)
-              *reinterpret_cast<uint4 *>(stage_b(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::arrive_at(tc::map_cta(&full[s], 0));
         }
       }
     }
@@ -304,7 +315,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           if ((G::F8 || kb == 0) && ai >= (uint32_t)NACC &&
               !(ok = warp_wait(&acc_empty[ab], ((ai / NACC) - 1) & 1, P.status)))
             break;
-          if (!(ok = warp_wait(&full[s], (qi / SQ) & 1, P.status))) break;
+          const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
+          if (!(ok = warp_wait(&full[s], (qi / SQ) & 1, P.status, cut))) break;
           tc::fence_after();
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
@@ -328,6 +340,28 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       if (tc::elect_one()) tc::commit_cg<CG>(drain);
       __syncwarp();
       warp_wait(drain, 0, P.status);
+    }
+  } else if (warp == 3) {
+    // ============================================================ rows of the next expert (GG_DW)
+    // A warp of its own, because the copies have to land first: the producer would lose that time for every tile.
+    if constexpr (MODE == GG_DW) {
+      uint32_t q0 = 0, phase = 0;  // phase: bit s, the use of tail[s]
+      for (int w = unit0; ok && tiles.get(w, t); w += units) {
+        const int nk = steps(t), left = t.rows & 63;
+        q0 += nk;
+        if (!(left & 15)) continue;
+        const int s = (q0 - 1) % SQ, to = (left + 15) & ~15, nbox = (mma_n(t) / CG + 63) / 64;
+        if (!(ok = warp_wait(&tail[s], phase >> s & 1, P.status))) break;
+        phase ^= 1u << s;
+        for (int i = lane; i < (to - left) * 8; i += 32) {
+          const int off = (left + i / 8) * 128 + (i % 8) * 16;  // whole rows: the swizzle stays inside a row
+          for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4 *>(stage_a(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < nbox; ++j) *reinterpret_cast<uint4 *>(stage_b(s) + j * 8192 + off) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::arrive_at(tc::map_cta(&full[s], 0));
+      }
     }
   } else if (warp >= kFirstEpw) {
     // ============================================================ epilogue
@@ -494,6 +528,7 @@ cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
 }  // namespace
 
 int grouped_tile_cols(GroupedKernel k) { return k == GG_WIDE ? Wide::BN : Narrow::BN; }
+int grouped_box_rows(GroupedKernel k) { return k == GG_WIDE ? Wide::BOX_ROWS : Narrow::BOX_ROWS; }
 int grouped_tile_lanes(GroupedKernel k) { return k == GG_WIDE ? Wide::LANES : Narrow::LANES; }
 
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,

@@ -41,6 +41,7 @@ enum GroupedKernel { GG_NARROW = 0, GG_WIDE = 1 };
 // Rows of the output (TMEM columns) and lanes per tile of each kernel.
 int grouped_tile_cols(GroupedKernel k);
 int grouped_tile_lanes(GroupedKernel k);
+int grouped_box_rows(GroupedKernel k);  // of the row operand's tensor map
 // fp8 != 0: e4m3 operands with block scales (GG_FWD only).
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream);
