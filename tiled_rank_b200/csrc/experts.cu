@@ -249,8 +249,8 @@ tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q,
   a.C = p->C;
   a.dtype = p->dtype;
   a.swiglu = p->swiglu;
-  a.vec_x = (p->T <= 1 || ld_x * es % 16 == 0) && (!p->swiglu || (long long)p->C * es % 16 == 0);
-  a.vec_q = p->R <= 1 || ld_q % 8 == 0;
+  a.vec = p->C % 8 == 0 && (p->T <= 1 || ld_x * es % 16 == 0) && (!p->swiglu || (long long)p->C * es % 16 == 0) &&
+          (p->R <= 1 || ld_q % 8 == 0);
   return launch_quant_rows(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILEQ_OK : TILEQ_ERR_CUDA;
 }
 
@@ -278,8 +278,8 @@ tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, v
   a.nO = (int)div_up(g->d_out, 128);
   a.nI = (int)div_up(g->d_in, 128);
   a.dtype = g->dtype;
-  a.vec_w = a.ld_w * es % 16 == 0 && (g->E == 1 || a.stride_w * es % 16 == 0);
-  a.vec_q = a.ld_q % 8 == 0 && (g->E == 1 || a.stride_q % 8 == 0);
+  a.vec = a.d_in % 8 == 0 && a.ld_w * es % 16 == 0 && a.ld_q % 8 == 0 &&
+          (g->E == 1 || (a.stride_w * es % 16 == 0 && a.stride_q % 8 == 0));
   const long long blocks = (long long)g->E * a.nO * a.nI;
   if (blocks > 0x7fffffff) return TILEQ_ERR_UNSUPPORTED;
   return launch_quant_weights(a, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILEQ_OK

@@ -17,44 +17,60 @@
 namespace tileq {
 namespace {
 
-// Eight consecutive values, widened; past `n` of them (or unaligned) one by one, zeros behind the end.
-__device__ __forceinline__ void load8(const void *base, long long at, int n, int dtype, bool vec, float (&v)[8]) {
-  if (vec && n >= 8) {
-    if (dtype == TILEQ_DT_F32) {
-      const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + at);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + at));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive values as loaded (two 16-byte words of fp32, one of 16 bits), and widened.
+template <int DT>
+struct Raw8 {
+  uint4 w[DT == TILEQ_DT_F32 ? 2 : 1];
+};
+// VEC: one or two 16-byte loads where `live`; else value by value, `n` of them.  Zeros behind the end.
+template <int DT, bool VEC>
+__device__ __forceinline__ Raw8<DT> load8(const void *base, long long at, int n) {
+  Raw8<DT> r;
+  if constexpr (VEC) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + at * (DT == TILEQ_DT_F32 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 f;
-        if (dtype == TILEQ_DT_BF16) {
-          f.x = __uint_as_float(w[i] << 16);
-          f.y = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-          f = __half22float2(u32_as_h2(w[i]));
-        }
+    for (int i = 0; i < (DT == TILEQ_DT_F32 ? 2 : 1); ++i) r.w[i] = n > 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  } else {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0;
+      if (i < n)
+        v[i] = DT == TILEQ_DT_F32 ? reinterpret_cast<const uint32_t *>(base)[at + i]
+                                  : reinterpret_cast<const uint16_t *>(base)[at + i];
+    }
+    if constexpr (DT == TILEQ_DT_F32) {
+      r.w[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      r.w[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    } else {
+      r.w[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen(const Raw8<DT> &r, float (&v)[8]) {
+  if constexpr (DT == TILEQ_DT_F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i] = __uint_as_float(r.w[i].x);
+      v[4 * i + 1] = __uint_as_float(r.w[i].y);
+      v[4 * i + 2] = __uint_as_float(r.w[i].z);
+      v[4 * i + 3] = __uint_as_float(r.w[i].w);
+    }
+  } else {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == TILEQ_DT_BF16) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(u32_as_h2(w[i]));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
       }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float f = 0.f;
-    if (i < n) {
-      if (dtype == TILEQ_DT_F32)
-        f = reinterpret_cast<const float *>(base)[at + i];
-      else if (dtype == TILEQ_DT_BF16)
-        f = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[at + i]);
-      else
-        f = __half2float(reinterpret_cast<const __half *>(base)[at + i]);
-    }
-    v[i] = f;
   }
 }
 
@@ -85,24 +101,27 @@ __device__ __forceinline__ uint2 round8(const float (&v)[8], float inv) {
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
-__device__ __forceinline__ void store8(uint8_t *q, int n, bool vec, uint2 w) {
-  if (vec && n >= 8) {
-    *reinterpret_cast<uint2 *>(q) = w;
-    return;
-  }
-  const unsigned long long b = (unsigned long long)w.y << 32 | w.x;
+template <bool VEC>
+__device__ __forceinline__ void store8(uint8_t *q, int n, uint2 w) {
+  if constexpr (VEC) {
+    if (n > 0) *reinterpret_cast<uint2 *>(q) = w;
+  } else {
+    const unsigned long long b = (unsigned long long)w.y << 32 | w.x;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) q[i] = (uint8_t)(b >> 8 * i);
+    for (int i = 0; i < 8; ++i)
+      if (i < n) q[i] = (uint8_t)(b >> 8 * i);
+  }
 }
 
 constexpr int kQRows = 8;    // rows of a CTA, a warp each
-constexpr int kQCols = 1024; // columns of a CTA: four loads of 16 bytes in flight per lane
+constexpr int kQCols = 1024; // columns of a CTA: four 16-byte loads a lane, issued before the first is used
+constexpr int kQU = kQCols / 256;
 
 // A warp reads 256 columns at a time, 16 lanes a block of 128.  The scales of
 // eight rows leave together: neighbouring rows are neighbours in a scale row, and
 // single 4-byte stores would each cost a 32-byte sector.
-template <bool SWIGLU>
+// VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
+template <int DT, bool SWIGLU, bool VEC>
 __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRowsArgs P) {
   __shared__ float sc[kQCols / 128][kQRows];
   pdl_wait_and_release();
@@ -113,37 +132,34 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
     const long long src = P.rows ? P.rows[r] : r;
     const bool live = src >= 0 && src < P.T;  // a row number outside x is padding: a row of zeros
     const float w = P.row_scale ? P.row_scale[r] : 1.f;
-    float v[kQCols / 256][8];
+    Raw8<DT> raw[kQU], up[SWIGLU ? kQU : 1];
 #pragma unroll
-    for (int u = 0; u < kQCols / 256; ++u) {
+    for (int u = 0; u < kQU; ++u) {
       const int c = c0 + u * 256 + lane * 8;
-      load8(P.x, src * P.ld_x + c, live ? P.C - c : 0, P.dtype, P.vec_x, v[u]);
+      raw[u] = load8<DT, VEC>(P.x, src * P.ld_x + c, live ? P.C - c : 0);
+      if constexpr (SWIGLU) up[u] = load8<DT, VEC>(P.x, src * P.ld_x + P.C + c, live ? P.C - c : 0);
     }
-    if constexpr (SWIGLU) {
 #pragma unroll
-      for (int u = 0; u < kQCols / 256; ++u) {
-        const int c = c0 + u * 256 + lane * 8;
-        float up[8];
-        load8(P.x, src * P.ld_x + P.C + c, live ? P.C - c : 0, P.dtype, P.vec_x, up);
+    for (int u = 0; u < kQU; ++u) {
+      const int c = c0 + u * 256 + lane * 8;
+      float v[8];
+      widen<DT>(raw[u], v);
+      if constexpr (SWIGLU) {
+        float b[8];
+        widen<DT>(up[u], b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] / (1.f + expf(-v[u][i])) * up[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * b[i];
       }
-    }
-    if (P.row_scale && live) {
+      if (P.row_scale && live) {
 #pragma unroll
-      for (int u = 0; u < kQCols / 256; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] *= w;
-    }
-#pragma unroll
-    for (int u = 0; u < kQCols / 256; ++u) {
-      const int c = c0 + u * 256 + lane * 8;
-      uint32_t m = amax8(v[u]);
+        for (int i = 0; i < 8; ++i) v[i] *= w;
+      }
+      uint32_t m = amax8(v);
 #pragma unroll
       for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       float inv;
       const float s = scale_of(m, inv);
-      store8(P.q + r * P.ld_q + c, P.C - c, P.vec_q, round8(v[u], inv));
+      store8<VEC>(P.q + r * P.ld_q + c, P.C - c, round8(v, inv));
       if ((lane & 15) == 0) sc[u * 2 + (lane >> 4)][warp] = s;
     }
   }
@@ -155,18 +171,24 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
 }
 
 // One CTA per 128 x 128 block, 64 values a thread.
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsArgs P) {
   __shared__ uint32_t top[8];
   pdl_wait_and_release();
   const long long per = (long long)P.nO * P.nI;
   const int e = (int)(blockIdx.x / per), b = (int)(blockIdx.x % per);
   const int o0 = b / P.nI * 128 + (int)(threadIdx.x >> 4), c = b % P.nI * 128 + (int)(threadIdx.x & 15) * 8;
+  Raw8<DT> raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int o = o0 + 16 * i;
+    raw[i] = load8<DT, VEC>(P.w, e * P.stride_w + o * P.ld_w + c, o < P.d_out ? P.d_in - c : 0);
+  }
   float v[8][8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int o = o0 + 16 * i;
-    load8(P.w, e * P.stride_w + o * P.ld_w + c, o < P.d_out ? P.d_in - c : 0, P.dtype, P.vec_w, v[i]);
+    widen<DT>(raw[i], v[i]);
     m = max(m, amax8(v[i]));
   }
 #pragma unroll
@@ -180,24 +202,39 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int o = o0 + 16 * i;
-    if (o < P.d_out) store8(P.q + e * P.stride_q + o * P.ld_q + c, P.d_in - c, P.vec_q, round8(v[i], inv));
+    if (o < P.d_out) store8<VEC>(P.q + e * P.stride_q + o * P.ld_q + c, P.d_in - c, round8(v[i], inv));
   }
   if (threadIdx.x == 0) P.scales[blockIdx.x] = s;
+}
+
+template <int DT>
+void (*rows_kernel(bool swiglu, bool vec))(const QuantRowsArgs) {
+  if (swiglu) return vec ? quant_rows_kernel<DT, true, true> : quant_rows_kernel<DT, true, false>;
+  return vec ? quant_rows_kernel<DT, false, true> : quant_rows_kernel<DT, false, false>;
+}
+template <int DT>
+void (*weights_kernel(bool vec))(const QuantWeightsArgs) {
+  return vec ? quant_weights_kernel<DT, true> : quant_weights_kernel<DT, false>;
 }
 
 }  // namespace
 
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.R + kQRows - 1) / kQRows), (unsigned)((a.C + kQCols - 1) / kQCols));
-  const cudaError_t e = launch_pdl(a.swiglu ? quant_rows_kernel<true> : quant_rows_kernel<false>, grid,
-                                   dim3(kQRows * 32), 0, stream, a);
+  const auto kern = a.dtype == TILEQ_DT_F32    ? rows_kernel<TILEQ_DT_F32>(a.swiglu, a.vec)
+                    : a.dtype == TILEQ_DT_BF16 ? rows_kernel<TILEQ_DT_BF16>(a.swiglu, a.vec)
+                                               : rows_kernel<TILEQ_DT_F16>(a.swiglu, a.vec);
+  const cudaError_t e = launch_pdl(kern, grid, dim3(kQRows * 32), 0, stream, a);
   if (e != cudaSuccess) return e;
   count_launches();
   return cudaGetLastError();
 }
 
 cudaError_t launch_quant_weights(const QuantWeightsArgs &a, int blocks, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(quant_weights_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  const auto kern = a.dtype == TILEQ_DT_F32    ? weights_kernel<TILEQ_DT_F32>(a.vec)
+                    : a.dtype == TILEQ_DT_BF16 ? weights_kernel<TILEQ_DT_BF16>(a.vec)
+                                               : weights_kernel<TILEQ_DT_F16>(a.vec);
+  const cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   count_launches();
   return cudaGetLastError();

@@ -13,7 +13,7 @@ struct QuantRowsArgs {
   long long ld_x, ld_q, ld_s;
   long long R, T;
   int C, dtype, swiglu;
-  int vec_x, vec_q;        // rows allow 16-byte loads, 8-byte stores
+  int vec;                 // the width is a multiple of 8, rows allow 16-byte loads and 8-byte stores
 };
 
 struct QuantWeightsArgs {
@@ -21,7 +21,7 @@ struct QuantWeightsArgs {
   uint8_t *q;
   float *scales;           // [E][nO][nI]
   long long ld_w, stride_w, ld_q, stride_q;
-  int d_out, d_in, nO, nI, dtype, vec_w, vec_q;
+  int d_out, d_in, nO, nI, dtype, vec;
 };
 
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t stream);
