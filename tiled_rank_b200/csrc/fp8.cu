@@ -121,8 +121,49 @@ constexpr int kQU = kQCols / 256;
 // eight rows leave together: neighbouring rows are neighbours in a scale row, and
 // single 4-byte stores would each cost a 32-byte sector.
 // VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
-template <int DT, bool SWIGLU, bool VEC>
+// What a value goes through is what the gathered case pays for: x comes from L2
+// for all but the first of a token's rows, so it is bound by instructions, not by
+// HBM.  16-bit values without a factor therefore stay in pairs: the maxima of two
+// blocks travel through the shuffles in the halves of one register, and bf16 is
+// scaled before it is widened (exact: a power of two; below bf16's normal range
+// the result is zero in e4m3 either way).
+enum QuantKind { Q_PLAIN = 0, Q_FACTOR = 1, Q_SWIGLU = 2 };
+
+// Maxima of the magnitudes of two loads (16-bit bit patterns, NaN on top): low half a's, high half b's.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_pair(const Raw8<DT> &a, const Raw8<DT> &b) {
+  const auto top = [](const uint4 &w) {
+    const uint32_t k = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+  };
+  const uint32_t x = top(a.w[0]), y = top(b.w[0]);
+  return __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+}
+
+template <int DT>
+__device__ __forceinline__ uint2 round8_pairs(const Raw8<DT> &r, float inv) {
+  if constexpr (DT == TILEQ_DT_BF16) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(inv);
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), f);
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(&p);
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)),
+                                      __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  } else {
+    float v[8];
+    widen<DT>(r, v);
+    return round8(v, inv);
+  }
+}
+
+template <int DT, QuantKind KIND, bool VEC>
 __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRowsArgs P) {
+  constexpr bool SWIGLU = KIND == Q_SWIGLU, PAIRS = KIND == Q_PLAIN && DT != TILEQ_DT_F32;
   __shared__ float sc[kQCols / 128][kQRows];
   pdl_wait_and_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,7 +172,6 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
   if (r < P.R) {
     const long long src = P.rows ? P.rows[r] : r;
     const bool live = src >= 0 && src < P.T;  // a row number outside x is padding: a row of zeros
-    const float w = P.row_scale ? P.row_scale[r] : 1.f;
     Raw8<DT> raw[kQU], up[SWIGLU ? kQU : 1];
 #pragma unroll
     for (int u = 0; u < kQU; ++u) {
@@ -139,28 +179,47 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
       raw[u] = load8<DT, VEC>(P.x, src * P.ld_x + c, live ? P.C - c : 0);
       if constexpr (SWIGLU) up[u] = load8<DT, VEC>(P.x, src * P.ld_x + P.C + c, live ? P.C - c : 0);
     }
+    uint8_t *q = P.q + r * P.ld_q + c0 + lane * 8;
+    const int n = P.C - c0 - lane * 8;
+    if constexpr (PAIRS) {
 #pragma unroll
-    for (int u = 0; u < kQU; ++u) {
-      const int c = c0 + u * 256 + lane * 8;
-      float v[8];
-      widen<DT>(raw[u], v);
-      if constexpr (SWIGLU) {
-        float b[8];
-        widen<DT>(up[u], b);
+      for (int u = 0; u < kQU; u += 2) {
+        uint32_t m = amax_pair<DT>(raw[u], raw[u + 1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * b[i];
+        for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t top = h ? m >> 16 : m & 0xffffu;
+          float inv;
+          const float s = scale_of(DT == TILEQ_DT_BF16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half((uint16_t)top))), inv);
+          store8<VEC>(q + (u + h) * 256, n - (u + h) * 256, round8_pairs<DT>(raw[u + h], inv));
+          if ((lane & 15) == 0) sc[(u + h) * 2 + (lane >> 4)][warp] = s;
+        }
       }
-      if (P.row_scale && live) {
+    } else {
+      const float w = P.row_scale ? P.row_scale[r] : 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= w;
+      for (int u = 0; u < kQU; ++u) {
+        float v[8];
+        widen<DT>(raw[u], v);
+        if constexpr (SWIGLU) {
+          float b[8];
+          widen<DT>(up[u], b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * b[i];
+        }
+        if (KIND != Q_PLAIN && live) {  // rows of zeros stay zeros, whatever their factor
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= w;
+        }
+        uint32_t m = amax8(v);
+#pragma unroll
+        for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float inv;
+        const float s = scale_of(m, inv);
+        store8<VEC>(q + u * 256, n - u * 256, round8(v, inv));
+        if ((lane & 15) == 0) sc[u * 2 + (lane >> 4)][warp] = s;
       }
-      uint32_t m = amax8(v);
-#pragma unroll
-      for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      float inv;
-      const float s = scale_of(m, inv);
-      store8<VEC>(P.q + r * P.ld_q + c, P.C - c, round8(v, inv));
-      if ((lane & 15) == 0) sc[u * 2 + (lane >> 4)][warp] = s;
     }
   }
   __syncthreads();
@@ -207,10 +266,13 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
   if (threadIdx.x == 0) P.scales[blockIdx.x] = s;
 }
 
+template <int DT, QuantKind KIND>
+void (*rows_kernel(bool vec))(const QuantRowsArgs) {
+  return vec ? quant_rows_kernel<DT, KIND, true> : quant_rows_kernel<DT, KIND, false>;
+}
 template <int DT>
-void (*rows_kernel(bool swiglu, bool vec))(const QuantRowsArgs) {
-  if (swiglu) return vec ? quant_rows_kernel<DT, true, true> : quant_rows_kernel<DT, true, false>;
-  return vec ? quant_rows_kernel<DT, false, true> : quant_rows_kernel<DT, false, false>;
+void (*rows_kernel(const QuantRowsArgs &a))(const QuantRowsArgs) {
+  return a.swiglu ? rows_kernel<DT, Q_SWIGLU>(a.vec) : a.row_scale ? rows_kernel<DT, Q_FACTOR>(a.vec) : rows_kernel<DT, Q_PLAIN>(a.vec);
 }
 template <int DT>
 void (*weights_kernel(bool vec))(const QuantWeightsArgs) {
@@ -221,9 +283,9 @@ void (*weights_kernel(bool vec))(const QuantWeightsArgs) {
 
 cudaError_t launch_quant_rows(const QuantRowsArgs &a, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.R + kQRows - 1) / kQRows), (unsigned)((a.C + kQCols - 1) / kQCols));
-  const auto kern = a.dtype == TILEQ_DT_F32    ? rows_kernel<TILEQ_DT_F32>(a.swiglu, a.vec)
-                    : a.dtype == TILEQ_DT_BF16 ? rows_kernel<TILEQ_DT_BF16>(a.swiglu, a.vec)
-                                               : rows_kernel<TILEQ_DT_F16>(a.swiglu, a.vec);
+  const auto kern = a.dtype == TILEQ_DT_F32    ? rows_kernel<TILEQ_DT_F32>(a)
+                    : a.dtype == TILEQ_DT_BF16 ? rows_kernel<TILEQ_DT_BF16>(a)
+                                               : rows_kernel<TILEQ_DT_F16>(a);
   const cudaError_t e = launch_pdl(kern, grid, dim3(kQRows * 32), 0, stream, a);
   if (e != cudaSuccess) return e;
   count_launches();
