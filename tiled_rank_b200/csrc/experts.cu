@@ -117,7 +117,8 @@ tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const
   a.bf16 = g->dtype == TILEQ_DT_BF16;
   a.out_dtype = g->out_dtype;
   a.nL = (int)div_up(a.L, lanes);
-  a.pair_store = g->out_dtype != TILEQ_DT_F32 && a.L % 2 == 0 && a.ldo % 2 == 0 && a.out_stride % 2 == 0;
+  const auto all = [&](long long n) { return a.L % n == 0 && a.ldo % n == 0 && a.out_stride % n == 0; };
+  a.store_words = all(8) ? 8 : all(2) ? 2 : 1;  // out is 16-byte aligned
   const long long tiles = a.nL * (mode == GG_DW ? (long long)g->E * div_up(a.C, bn) : g->P / bn + std::min(g->E, g->P));
   if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
   if (!encode(&a.amap, oa, mode == GG_FWD ? 128 : 64) || !encode(&a.bmap, ob, mode == GG_DW ? 64 : grouped_box_rows(k)))

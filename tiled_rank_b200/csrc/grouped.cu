@@ -42,6 +42,7 @@
 namespace tileq {
 namespace {
 
+constexpr int kScaleGroup = 4;      // fp8: blocks whose scales the fold's warps stage at a time
 constexpr int kFirstEpw = 4;        // first epilogue warp
 constexpr int kRegsControl = 56, kRegsEpilogue = 224;  // registers a thread where the warps split them
 constexpr int kRowTileGroup = 8;    // column tiles that share a pass over the lane tiles
@@ -57,16 +58,22 @@ struct GCfg {
   static constexpr int COLS = BN / (EPW / 4);  // columns of one epilogue warp
   static constexpr int THREADS = (kFirstEpw + EPW) * 32;
   static constexpr bool SPLIT_REGS = F8 && BN == 256;
+  static constexpr int CHUNK = 16;  // fp8: columns of one TMEM load of the fold
+  static constexpr int SCALES = F8 ? 2 * kScaleGroup * BN * 4 : 0;
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = BN / CG * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TAB = (2 * kGroupedMaxE + 2) * 4;
-  static constexpr int SQ = (227 * 1024 - TAB - (F8 ? 2 * BN * 4 : 0) - 512) / STAGE;
+  static constexpr int SQ = (227 * 1024 - TAB - SCALES - 512) / STAGE;
+  // fp8: the columns of a wide tile are two MMAs with accumulators of their own, each folded by its own four
+  // epilogue warps: the fold of a part has the other part's MMA time on top of its next one's
+  static constexpr int PARTS = F8 && BN == 256 ? 2 : 1;
+  static constexpr int PC = BN / PARTS;  // columns of a part
   static constexpr int NACC = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = NACC * BN;
   static constexpr int BAR_OFF = SQ * STAGE;
-  static constexpr int SCALE_OFF = BAR_OFF + ((3 * SQ + 2 * NACC + 1) * 8 + 31) / 16 * 16;
-  static constexpr int TAB_OFF = SCALE_OFF + (F8 ? 2 * BN * 4 : 0);
+  static constexpr int SCALE_OFF = BAR_OFF + ((3 * SQ + 2 * NACC * PARTS + 1) * 8 + 31) / 16 * 16;
+  static constexpr int TAB_OFF = SCALE_OFF + SCALES;
   static constexpr int SMEM = TAB_OFF + TAB;
   static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two of tensor memory columns");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -104,14 +111,58 @@ struct Tiles {
   }
 };
 
-// 32 lanes x 16 columns into r; the values are there after wait16 of the same r.
-__device__ __forceinline__ void wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
+// TMEM to registers in the layout of 8 x 8 blocks (16x256b): of 32 lanes x 32
+// columns at taddr, r[h][4 j + 2 g + i] is lane 16 h + 8 g + id / 4, column
+// 8 j + 2 (id % 4) + i for thread id.  A thread so holds two neighbouring columns
+// of four lanes: a column's scale, wanted by every lane, is read from shared
+// memory once for four of them (one lane per thread would be bound by those
+// reads), and the block transposes with one instruction for the stores.
+// The values are there after wait_block of the same r.
+__device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
                : "memory");
 }
+template <int N>
+__device__ __forceinline__ void ld_block(uint32_t taddr, uint32_t (&r)[2][N]) {
+  ld_half(taddr, r[0]);
+  ld_half(taddr + (16u << 16), r[1]);
+}
+// (the registers pass through the asm, so that no use of them moves in front of the wait)
+__device__ __forceinline__ void tie(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+__device__ __forceinline__ void tie(uint32_t (&r)[16]) {
+  tie(*reinterpret_cast<uint32_t(*)[8]>(&r[0]));
+  tie(*reinterpret_cast<uint32_t(*)[8]>(&r[8]));
+}
+template <int N>
+__device__ __forceinline__ void wait_block(uint32_t (&r)[2][N]) {
+  tc::wait_ld();
+  tie(r[0]);
+  tie(r[1]);
+}
+// acc += v * s, two fp32 FMAs in one instruction
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t v, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // mbar_wait by a whole warp with one answer: no lane leaves a loop in which the others still meet.
 // (`remote`: the pair's other CTA has written memory before it arrived.)
@@ -129,61 +180,77 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Columns c .. c + 15 of this warp's 32 lanes, 16-bit results: lanes 2j and 2j + 1
-// exchange so that each stores two neighbouring outputs of one column (PAIR), else one by one.
-template <int DT, bool PAIR>
-__device__ __forceinline__ void store16_b16(uint16_t *out, long long ldo, int n, bool in, int odd, const float (&v)[16]) {
-  if constexpr (PAIR) {
-    out += odd ? ldo - 1 : 0;
+// Stores 8 columns (n of them exist) x 32 lanes (nl exist) to out + column * ldo + lane;
+// v[g]: this thread's two columns of lane 8 g + id / 4.  16-bit results are
+// transposed as 8 x 8 blocks, which leaves thread id the lanes 8 g + 2 (id % 4) + 0, 1
+// of column id / 4; WORDS is how much of them one store may take: 1 a value, 2 the
+// pair, 8 a run of eight lanes after a transposition among the four threads of a column.
+template <int DT, int WORDS>
+__device__ __forceinline__ void store_b16(uint16_t *out, long long ldo, int n, int nl, int id, const uint64_t (&v)[4]) {
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2, out += 2 * ldo) {
-      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-      const uint32_t w = pack2<DT>(odd ? got : v[i], odd ? v[i + 1] : got);
-      if (in && i + odd < n) *reinterpret_cast<uint32_t *>(out) = w;
-    }
+  for (int g = 0; g < 4; ++g)
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(w[g]) : "r"(pack2<DT>(low(v[g]), high(v[g]))));
+  const int q = id & 3;
+  out += (id >> 2) * ldo;
+  const bool in = (id >> 2) < n;
+  if constexpr (WORDS == 8) {
+    const bool b0 = q & 1, b1 = q & 2;
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, b0 ? w[0] : w[1], 1);
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? w[2] : w[3], 1);
+    const uint32_t a0 = b0 ? x : w[0], a1 = b0 ? w[1] : x, a2 = b0 ? y : w[2], a3 = b0 ? w[3] : y;
+    const uint32_t u = __shfl_xor_sync(0xffffffffu, b1 ? a0 : a2, 2);
+    const uint32_t z = __shfl_xor_sync(0xffffffffu, b1 ? a1 : a3, 2);
+    if (in && q * 8 < nl)
+      *reinterpret_cast<uint4 *>(out + q * 8) = b1 ? make_uint4(u, z, a2, a3) : make_uint4(a0, a1, u, z);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i, out += ldo)
-      if (in && i < n) *out = (uint16_t)pack2<DT>(v[i], 0.f);
+    for (int g = 0; g < 4; ++g) {
+      const int l = 8 * g + 2 * q;
+      if constexpr (WORDS == 2) {
+        if (in && l < nl) *reinterpret_cast<uint32_t *>(out + l) = w[g];
+      } else {
+        if (in && l < nl) out[l] = (uint16_t)w[g];
+        if (in && l + 1 < nl) out[l + 1] = (uint16_t)(w[g] >> 16);
+      }
+    }
   }
 }
-
-// Columns c .. c + 15 of this warp's 32 lanes (l: this thread's) to out + base + column * ldo + l.
-__device__ __forceinline__ void store16(const GroupedArgs &P, long long base, int c, int ncols, int l, int lane,
-                                        const float (&v)[16]) {
-  const bool in = l < P.L;
-  const int n = ncols - c, odd = lane & 1;
-  base += c * P.ldo + l;
-  if (P.out_dtype == TILEQ_DT_F32) {
-    float *out = reinterpret_cast<float *>(P.out) + base;
-#pragma unroll
-    for (int i = 0; i < 16; ++i, out += P.ldo)
-      if (in && i < n) *out = v[i];
-    return;
-  }
+template <int DT>
+__device__ __forceinline__ void store_b16(const GroupedArgs &P, long long base, int n, int nl, int id, const uint64_t (&v)[4]) {
   uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base;
-  if (P.out_dtype == TILEQ_DT_BF16) {
-    if (P.pair_store)
-      store16_b16<TILEQ_DT_BF16, true>(out, P.ldo, n, in, odd, v);
-    else
-      store16_b16<TILEQ_DT_BF16, false>(out, P.ldo, n, in, odd, v);
+  if (P.store_words == 8)
+    store_b16<DT, 8>(out, P.ldo, n, nl, id, v);
+  else if (P.store_words == 2)
+    store_b16<DT, 2>(out, P.ldo, n, nl, id, v);
+  else
+    store_b16<DT, 1>(out, P.ldo, n, nl, id, v);
+}
+__device__ __forceinline__ void store_block(const GroupedArgs &P, long long base, int n, int nl, int id, const uint64_t (&v)[4]) {
+  if (P.out_dtype == TILEQ_DT_F32) {
+    float *out = reinterpret_cast<float *>(P.out) + base + 2 * (id & 3) * P.ldo + (id >> 2);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (8 * g + (id >> 2) < nl) {
+        if (2 * (id & 3) < n) out[8 * g] = low(v[g]);
+        if (2 * (id & 3) + 1 < n) out[P.ldo + 8 * g] = high(v[g]);
+      }
+  } else if (P.out_dtype == TILEQ_DT_BF16) {
+    store_b16<TILEQ_DT_BF16>(P, base, n, nl, id, v);
   } else {
-    if (P.pair_store)
-      store16_b16<TILEQ_DT_F16, true>(out, P.ldo, n, in, odd, v);
-    else
-      store16_b16<TILEQ_DT_F16, false>(out, P.ldo, n, in, odd, v);
+    store_b16<TILEQ_DT_F16>(P, base, n, nl, id, v);
   }
 }
 
 template <class G, GroupedMode MODE>
 __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_constant__ GroupedArgs P) {
-  constexpr int CG = G::CG, SQ = G::SQ, NACC = G::NACC;
+  constexpr int CG = G::CG, SQ = G::SQ, NACC = G::NACC, PARTS = G::PARTS;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle wants tiles at multiples of 1024
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::BAR_OFF);
   uint64_t *empty = full + SQ;
   uint64_t *acc_full = empty + SQ;
-  uint64_t *acc_empty = acc_full + NACC;
-  uint64_t *tail = acc_empty + NACC;  // [SQ] GG_DW: the copies of a stage with foreign rows
+  uint64_t *acc_empty = acc_full + PARTS * NACC;  // both [PARTS][NACC]
+  uint64_t *tail = acc_empty + PARTS * NACC;  // [SQ] GG_DW: the copies of a stage with foreign rows
   uint64_t *drain = tail + SQ;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   float *scale = reinterpret_cast<float *>(smem + G::SCALE_OFF);
@@ -201,9 +268,9 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
     }
-    for (int b = 0; b < NACC; ++b) {
+    for (int b = 0; b < PARTS * NACC; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], G::EPW * CG);
+      mbar_init(&acc_empty[b], G::EPW / PARTS * CG);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -244,8 +311,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
 
   Tiles<G, MODE> tiles{first, beg, P.E, P.L, P.nL, P.C};
   auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
-  // columns of the tile's MMA
-  auto mma_n = [&](const Tile &t) { return (t.ncols + 16 * CG - 1) / (16 * CG) * (16 * CG); };
+  // columns of one part's MMA
+  auto mma_n = [&](const Tile &t) { return (t.ncols + 16 * CG * PARTS - 1) / (16 * CG * PARTS) * (16 * CG); };
   Tile t;
   bool ok = true;
 
@@ -260,7 +327,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
       constexpr int ABOX = MODE == GG_FWD ? 1 : 2;         // boxes of A: 128 rows, or twice 64 columns
       constexpr int BBOX = MODE == GG_DW ? 64 : G::BOX_ROWS;  // columns of the tile in one box of B
-      const int nbox = (half + BBOX - 1) / BBOX;
+      const int nbox = PARTS == 2 ? 2 : (half + BBOX - 1) / BBOX;
+      const int bstep = PARTS == 2 ? half * CG : BBOX;  // columns from one box to the next (two parts: a box each)
       const uint32_t bytes = G::A_BYTES + nbox * BBOX * 128;
       for (int kb = 0; kb < nk; ++kb, ++qi) {
         const int s = qi % SQ;
@@ -283,7 +351,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           int x, y, z = 0;
           if (MODE == GG_FWD || (MODE == GG_DX && !is_a)) {
             x = kb * G::KE;
-            y = is_a ? l0 : t.row0 + c0 + i * BBOX;
+            y = is_a ? l0 : t.row0 + c0 + i * bstep;
           } else {
             x = (is_a ? l0 : c0) + i * 64;
             y = (MODE == GG_DW ? t.row0 : 0) + kb * 64;
@@ -312,27 +380,32 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
                                ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
         for (int kb = 0; kb < nk; ++kb, ++qi) {
           const int s = qi % SQ, ab = ai % NACC;
-          if ((G::F8 || kb == 0) && ai >= (uint32_t)NACC &&
-              !(ok = warp_wait(&acc_empty[ab], ((ai / NACC) - 1) & 1, P.status)))
-            break;
           const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
           if (!(ok = warp_wait(&full[s], (qi / SQ) & 1, P.status, cut))) break;
-          tc::fence_after();
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
           const uint64_t ad = tc::sdesc(smem_addr(stage_a(s)), A_MN ? 8192 : 16);
           const uint64_t bd = tc::sdesc(smem_addr(stage_b(s)), B_MN ? 8192 : 16);
-          if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (MODE != GG_DW || kk < nmma)
-                tc::mma_ss<CG, G::F8>(tmem + ab * G::BN, ad + (uint64_t)(kk * (A_MN ? 128 : 2)),
-                                      bd + (uint64_t)(kk * (B_MN ? 128 : 2)), idesc,
-                                      (kk || (!G::F8 && kb)) ? 1u : 0u);
-            tc::commit_cg<CG>(&empty[s]);
-            if (G::F8 || kb == nk - 1) tc::commit_cg<CG>(&acc_full[ab]);
+          for (int part = 0; part < PARTS; ++part) {
+            const int pa = part * NACC + ab;
+            if ((G::F8 || kb == 0) && ai >= (uint32_t)NACC &&
+                !(ok = warp_wait(&acc_empty[pa], ((ai / NACC) - 1) & 1, P.status)))
+              break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (MODE != GG_DW || kk < nmma)
+                  tc::mma_ss<CG, G::F8>(tmem + pa * G::PC, ad + (uint64_t)(kk * (A_MN ? 128 : 2)),
+                                        bd + (uint64_t)(kk * (B_MN ? 128 : 2) + part * (8192 >> 4)), idesc,
+                                        (kk || (!G::F8 && kb)) ? 1u : 0u);
+              if (part == PARTS - 1) tc::commit_cg<CG>(&empty[s]);
+              if (G::F8 || kb == nk - 1) tc::commit_cg<CG>(&acc_full[pa]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (G::F8 || kb == nk - 1) ++ai;
         }
       }
@@ -369,15 +442,16 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     // (168 registers a thread at launch: 384 * 168 = 128 * (56 + 2 * 224))
     if constexpr (G::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsEpilogue));
     const int half = (warp - kFirstEpw) >> 2;
-    const int row = (warp & 3) * 32 + lane;  // TMEM lane quadrant of this warp
-    const uint32_t lane_addr = tc::lane_base(warp);
-    uint32_t ai = 0;
+    const uint32_t lane_addr = tc::lane_base(warp);  // TMEM lane quadrant of this warp
+    uint32_t ai = 0, gi = 0;
     // (fp8: the four warps of a named barrier stay together, also after a wait that gave up)
     for (int w = unit0; (ok || G::F8) && tiles.get(w, t); w += units) {
-      const int nk = steps(t), l = t.l0 + (int)rank * 128 + row;
-      const long long base = MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)t.c0 * P.ldo
-                                           : (long long)(t.row0 + t.c0) * P.ldo;
-      const int cw = half * G::COLS;  // first column of this warp
+      const int nk = steps(t), l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
+      const int cw = half * (PARTS == 2 ? mma_n(t) : G::COLS);              // first column of this warp
+      const int mine = min(t.ncols - cw, PARTS == 2 ? mma_n(t) : G::COLS);  // its columns, none if <= 0
+      const int nl = P.L - l0;
+      const long long base = (MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)(t.c0 + cw) * P.ldo
+                                            : (long long)(t.row0 + t.c0 + cw) * P.ldo) + l0;
       if constexpr (!G::F8) {
         const int ab = ai % NACC;
         if (nk > 0) {
@@ -385,20 +459,19 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           tc::fence_after();
         }
 #pragma unroll 1
-        for (int c = cw; c < min(cw + G::COLS, t.ncols); c += 32) {
+        for (int c = 0; c < mine; c += 32) {
           uint32_t r[2][16];
           if (nk > 0) {
-            tc::ld16_nowait(tmem + lane_addr + ab * G::BN + c, r[0]);
-            tc::ld16_nowait(tmem + lane_addr + ab * G::BN + c + 16, r[1]);
-            wait16(r[0]);
-            wait16(r[1]);
+            ld_block(tmem + lane_addr + ab * G::BN + cw + c, r);
+            wait_block(r);
           }
-          float v[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int j = 0; j < 4; ++j) {
+            uint64_t v[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = nk > 0 ? __uint_as_float(r[h][i]) : 0.f;  // an expert without rows
-            store16(P, base, c + 16 * h, t.ncols, l, lane, v);
+            for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
+              v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
+            store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
           }
         }
         if (nk > 0) {
@@ -408,60 +481,72 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           ++ai;
         }
       } else {
-        float acc[G::COLS];
+        constexpr int CH = G::CHUNK, NCH = G::COLS / CH, GROUPS = CH / 8;
+        uint64_t acc[G::COLS / 8][4];  // [8 columns][lane block]: two columns, folded by one packed FMA
 #pragma unroll
-        for (int i = 0; i < G::COLS; ++i) acc[i] = 0.f;
+        for (int i = 0; i < G::COLS / 8; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) acc[i][g] = 0;
+        const int part = PARTS == 2 ? half : 0, col0 = PARTS == 2 ? 0 : cw;
+        // scales of kScaleGroup blocks at a time: thread tid's column (the last one where it has none) and block,
+        // fetched while the group before is folded
         const int tid = threadIdx.x & 127;  // within the four warps that share these columns
-        const bool has = tid < G::COLS && cw + tid < t.ncols;
-        const float *xs = P.xs + t.row0 + t.c0 + cw + tid;
+        const float *xs = P.xs + t.row0 + t.c0 + (mine > 0 ? cw + min(tid, mine - 1) : 0);
         const float *ws = P.ws + ((long long)t.e * P.nLb + min((t.l0 + (int)rank * 128) / 128, P.nLb - 1)) * P.nKb;
-        float sx = has ? __ldg(xs) : 0.f, sw = __ldg(ws);
-        for (int kb = 0; kb < nk; ++kb, ++ai) {
-          const int ab = ai % NACC;
-          float *sc = scale + (ai & 1) * G::BN + cw;
-          if (tid < G::COLS) sc[tid] = sx * sw;
-          if (kb + 1 < nk) {
-            sx = has ? __ldg(xs + (long long)(kb + 1) * P.ld_xs) : 0.f;
-            sw = __ldg(ws + kb + 1);
+        float sx[kScaleGroup], sw[kScaleGroup];
+        auto fetch = [&](int kb) {
+#pragma unroll
+          for (int j = 0; j < kScaleGroup; ++j) {
+            const int k = min(kb + j, nk - 1);
+            sx[j] = __ldg(xs + k * P.ld_xs);
+            sw[j] = __ldg(ws + k);
           }
-          // also keeps these warps within one block of each other: two scale buffers do
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int kg = 0; kg < nk; kg += kScaleGroup) {
+          float *sc = scale + (gi++ & 1) * kScaleGroup * G::BN + half * G::COLS;
+          if (G::COLS == 128 || tid < G::COLS) {
+#pragma unroll
+            for (int j = 0; j < kScaleGroup; ++j) sc[j * G::BN + tid] = sx[j] * sw[j];
+          }
+          fetch(kg + kScaleGroup);
+          // also keeps these warps within one group of each other: two buffers of scales do
           named_sync(1 + half, 128);
-          ok = ok && warp_wait(&acc_full[ab], (ai / NACC) & 1, P.status);
-          tc::fence_after();
-          const uint32_t ta = tmem + lane_addr + ab * G::BN + cw;
-          constexpr int NCH = G::COLS / 16;
-          uint32_t r[2][16];
-          if (cw < t.ncols) {
-            tc::ld16_nowait(ta, r[0]);
+          sc += 2 * (lane & 3);
+#pragma unroll 1
+          for (int kb = kg; kb < min(kg + kScaleGroup, nk); ++kb, ++ai, sc += G::BN) {
+            const int pa = part * NACC + ai % NACC;
+            ok = ok && warp_wait(&acc_full[pa], (ai / NACC) & 1, P.status);
+            tc::fence_after();
+            const uint32_t ta = tmem + lane_addr + pa * G::PC + col0;
+            uint32_t r[2][2][CH / 2];
+            if (mine > 0) {
+              ld_block(ta, r[0]);
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-              if (cw + ch * 16 < t.ncols) {
-                wait16(r[ch & 1]);
-                if (ch + 1 < NCH && cw + (ch + 1) * 16 < t.ncols) tc::ld16_nowait(ta + (ch + 1) * 16, r[(ch + 1) & 1]);
+              for (int ch = 0; ch < NCH; ++ch) {
+                if (ch * CH < mine) {
+                  wait_block(r[ch & 1]);
+                  if (ch + 1 < NCH && (ch + 1) * CH < mine) ld_block(ta + (ch + 1) * CH, r[(ch + 1) & 1]);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                  const float4 f = *reinterpret_cast<const float4 *>(sc + ch * 16 + i);
-                  acc[ch * 16 + i] = fmaf(__uint_as_float(r[ch & 1][i]), f.x, acc[ch * 16 + i]);
-                  acc[ch * 16 + i + 1] = fmaf(__uint_as_float(r[ch & 1][i + 1]), f.y, acc[ch * 16 + i + 1]);
-                  acc[ch * 16 + i + 2] = fmaf(__uint_as_float(r[ch & 1][i + 2]), f.z, acc[ch * 16 + i + 2]);
-                  acc[ch * 16 + i + 3] = fmaf(__uint_as_float(r[ch & 1][i + 3]), f.w, acc[ch * 16 + i + 3]);
+                  for (int j = 0; j < GROUPS; ++j) {
+                    const uint64_t s = *reinterpret_cast<const uint64_t *>(sc + ch * CH + 8 * j);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                      fma2(acc[ch * GROUPS + j][g],
+                           pair(r[ch & 1][g >> 1][4 * j + 2 * (g & 1)], r[ch & 1][g >> 1][4 * j + 2 * (g & 1) + 1]), s);
+                  }
                 }
               }
             }
-          }
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[ab], 0));
-        }
-#pragma unroll
-        for (int ch = 0; ch < G::COLS / 16; ++ch) {
-          if (ok && cw + ch * 16 < t.ncols) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = acc[ch * 16 + i];
-            store16(P, base, cw + ch * 16, t.ncols, l, lane, v);
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[pa], 0));
           }
         }
+#pragma unroll
+        for (int j = 0; j < G::COLS / 8; ++j)
+          if (ok && 8 * j < mine) store_block(P, base + 8 * j * P.ldo, mine - 8 * j, nl, lane, acc[j]);
       }
     }
   }

@@ -28,7 +28,7 @@ struct GroupedArgs {
   int bf16;                // 16-bit operands: 1 bf16, 0 fp16
   void *out;
   int out_dtype;           // TILEQ_DT_*
-  int pair_store;          // two neighbouring outputs of 16 bits may be stored as one word
+  int store_words;         // 16-bit results that one store may take: 1, 2 or 8 neighbours
   long long ldo, out_stride;
   const float *xs;         // fp8: scales of the rows [R / 128][ld_xs], of the weights [E][nLb][nKb]
   const float *ws;
