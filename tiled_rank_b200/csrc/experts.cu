@@ -101,27 +101,33 @@ tileq_status check(const tileq_grouped *g, const void *a, const void *b, const v
 // The wide kernel (pairs of CTAs, 256 x 256 tiles) needs experts with enough
 // rows to fill its columns; the narrow one (one CTA, 128 x 64) streams the
 // weights of experts with few rows.
-GroupedKernel pick(GroupedMode mode, const tileq_grouped *g) {
+GroupedKernel pick(GroupedMode mode, const tileq_grouped *g, bool fp8) {
   if (mode == GG_DW) return GG_WIDE;
   const long long live = std::min(g->E, std::max(g->P, 1));
-  return g->P > 48 * live ? GG_WIDE : GG_NARROW;
+  return g->P > (fp8 ? 96 : 48) * live ? GG_WIDE : GG_NARROW;
 }
 
-tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const Operand &oa, const Operand &ob,
-                 bool fp8, cudaStream_t stream) {
-  const GroupedKernel k = pick(mode, g);
+// contig: the contiguous output dimension; weights and rows: the operands.  The rows' operand lies on the TMEM
+// columns, but for the wide fp8 kernel; GG_DW has no weights among its operands, `weights` is x.
+tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const Operand &weights, const Operand &rows,
+                 int contig, bool fp8, cudaStream_t stream) {
+  const GroupedKernel k = pick(mode, g, fp8);
+  const bool on_lanes = fp8 && k == GG_WIDE;
   const int bn = grouped_tile_cols(k), lanes = grouped_tile_lanes(k), cg = lanes / 128;
   a.offsets = g->expert_offsets;
   a.E = g->E;
   a.P = g->P;
+  a.L = contig;
+  a.C = mode == GG_DW ? g->d_out : contig;
   a.bf16 = g->dtype == TILEQ_DT_BF16;
   a.out_dtype = g->out_dtype;
-  a.nL = (int)div_up(a.L, lanes);
-  const auto all = [&](long long n) { return a.L % n == 0 && a.ldo % n == 0 && a.out_stride % n == 0; };
+  const auto all = [&](long long n) { return contig % n == 0 && a.ldo % n == 0 && a.out_stride % n == 0; };
   a.store_words = all(8) ? 8 : all(2) ? 2 : 1;  // out is 16-byte aligned
-  const long long tiles = a.nL * (mode == GG_DW ? (long long)g->E * div_up(a.C, bn) : g->P / bn + std::min(g->E, g->P));
+  const long long row_tiles = g->P / (on_lanes ? lanes : bn) + std::min(g->E, g->P);  // at most
+  const long long tiles = div_up(contig, on_lanes ? bn : lanes) * (mode == GG_DW ? g->E * div_up(a.C, bn) : row_tiles);
   if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
-  if (!encode(&a.amap, oa, mode == GG_FWD ? 128 : 64) || !encode(&a.bmap, ob, mode == GG_DW ? 64 : grouped_box_rows(k)))
+  if (!encode(&a.amap, on_lanes ? rows : weights, mode == GG_FWD ? 128 : 64) ||
+      !encode(&a.bmap, on_lanes ? weights : rows, mode == GG_DW ? 64 : grouped_box_rows(k)))
     return TILEQ_ERR_CUDA;
   const int sms = sm_count();
   if (sms < cg) return TILEQ_ERR_CUDA;
@@ -147,13 +153,12 @@ tileq_status tileq_grouped_gemm(const tileq_grouped *g, const void *x, const voi
   if (g->P == 0) return TILEQ_OK;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.L = g->d_out;
   a.R = g->d_in;
   a.out = y;
   a.ldo = s.y;
   a.status = static_cast<int *>(ws);
   return run(a, GG_FWD, g, {w, g->dtype, g->d_in, g->d_out, g->E, s.w, s.we}, {x, g->dtype, g->d_in, g->P, 0, s.x, 0},
-             false, reinterpret_cast<cudaStream_t>(stream));
+             g->d_out, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const void *w, void *dx, void *ws,
@@ -167,13 +172,12 @@ tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const
   if (g->P == 0) return TILEQ_OK;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.L = g->d_in;
   a.R = g->d_out;
   a.out = dx;
   a.ldo = s.x;
   a.status = static_cast<int *>(ws);
   return run(a, GG_DX, g, {w, g->dtype, g->d_in, g->d_out, g->E, s.w, s.we}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0},
-             false, reinterpret_cast<cudaStream_t>(stream));
+             g->d_in, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const void *dy, void *dw, void *ws,
@@ -186,14 +190,12 @@ tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const 
   if (s.x % 8 || s.y % 8) return TILEQ_ERR_UNSUPPORTED;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.L = g->d_in;
-  a.C = g->d_out;
   a.out = dw;
   a.ldo = s.w;
   a.out_stride = s.we;
   a.status = static_cast<int *>(ws);
-  return run(a, GG_DW, g, {x, g->dtype, g->d_in, g->P, 0, s.x, 0}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0}, false,
-             reinterpret_cast<cudaStream_t>(stream));
+  return run(a, GG_DW, g, {x, g->dtype, g->d_in, g->P, 0, s.x, 0}, {dy, g->dtype, g->d_out, g->P, 0, s.y, 0},
+             g->d_in, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float *xs, int64_t ld_xs, const void *wq,
@@ -209,18 +211,17 @@ tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float 
   if (g->P == 0) return TILEQ_OK;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.L = g->d_out;
   a.R = g->d_in;
   a.out = y;
   a.ldo = s.y;
   a.xs = xs;
   a.ws = w_scales;
   a.ld_xs = ld_xs ? ld_xs : g->P;
-  a.nLb = (int)div_up(g->d_out, 128);
+  a.nOb = (int)div_up(g->d_out, 128);
   a.nKb = (int)div_up(g->d_in, 128);
   a.status = static_cast<int *>(ws);
   return run(a, GG_FWD, g, {wq, TILEQ_DT_E4M3, g->d_in, g->d_out, g->E, s.w, s.we},
-             {xq, TILEQ_DT_E4M3, g->d_in, g->P, 0, s.x, 0}, true, reinterpret_cast<cudaStream_t>(stream));
+             {xq, TILEQ_DT_E4M3, g->d_in, g->P, 0, s.x, 0}, g->d_out, true, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q, float *scales,

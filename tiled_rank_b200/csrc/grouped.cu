@@ -29,8 +29,12 @@
 //   4..    epilogue: TMEM to registers, one rounding, stores.
 // fp8: one 128-byte stage is one scale block.  Every block gets an accumulator
 // of its own, which the epilogue warps fold into fp32 registers with
-// xs[block][row] * ws[e][l / 128][block]: one FMA per product of sums, as the
+// xs[block][row] * ws[e][o / 128][block]: one FMA per sum and block, as the
 // scales are no powers of two in general and cannot be left to the exponent.
+// In the narrow kernel a column's scale is read from shared memory; wide tiles
+// are too many columns for that (the reads alone cost more than the MMAs), so
+// there the operands change places: rows of x on the lanes (ROWS), each thread
+// with the scale of its own row in a register.
 // Every wait is bounded and reports TILEQ_ERR_TIMEOUT.
 #include "grouped.cuh"
 
@@ -42,7 +46,7 @@
 namespace tileq {
 namespace {
 
-constexpr int kScaleGroup = 4;      // fp8: blocks whose scales the fold's warps stage at a time
+constexpr int kScaleGroup = 8;      // narrow fp8: blocks whose scales the fold's warps stage at a time
 constexpr int kFirstEpw = 4;        // first epilogue warp
 constexpr int kRegsControl = 56, kRegsEpilogue = 224;  // registers a thread where the warps split them
 constexpr int kRowTileGroup = 8;    // column tiles that share a pass over the lane tiles
@@ -51,23 +55,23 @@ template <int CG_, int BN_, bool F8_>
 struct GCfg {
   static constexpr int CG = CG_, BN = BN_;
   static constexpr bool F8 = F8_;
+  static constexpr bool ROWS = F8 && BN == 256;  // the experts' rows on the lanes, d_out on the columns
   static constexpr int LANES = 128 * CG;
   static constexpr int KE = F8 ? 128 : 64;  // reduction elements per stage (128 bytes)
-  static constexpr int BOX_ROWS = BN == 256 ? 64 : 32;  // rows of one box of a row operand (B of GG_FWD, GG_DX)
+  static constexpr int BOX_B = BN == 256 ? 64 : 32;  // rows of one box of B where the reduction is contiguous
   static constexpr int EPW = BN == 256 ? 8 : 4;
   static constexpr int COLS = BN / (EPW / 4);  // columns of one epilogue warp
   static constexpr int THREADS = (kFirstEpw + EPW) * 32;
-  static constexpr bool SPLIT_REGS = F8 && BN == 256;
-  static constexpr int CHUNK = 16;  // fp8: columns of one TMEM load of the fold
-  static constexpr int SCALES = F8 ? 2 * kScaleGroup * BN * 4 : 0;
+  static constexpr bool SPLIT_REGS = ROWS;
+  static constexpr int SCALES = F8 && !ROWS ? 2 * kScaleGroup * BN * 4 : 0;
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = BN / CG * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TAB = (2 * kGroupedMaxE + 2) * 4;
   static constexpr int SQ = (227 * 1024 - TAB - SCALES - 512) / STAGE;
-  // fp8: the columns of a wide tile are two MMAs with accumulators of their own, each folded by its own four
-  // epilogue warps: the fold of a part has the other part's MMA time on top of its next one's
-  static constexpr int PARTS = F8 && BN == 256 ? 2 : 1;
+  // ROWS: the columns of a tile are two MMAs, one for each 128 of d_out and so for each weight scale, with
+  // accumulators of their own, folded by four epilogue warps each: while one part is folded the other's MMAs run
+  static constexpr int PARTS = ROWS ? 2 : 1;
   static constexpr int PC = BN / PARTS;  // columns of a part
   static constexpr int NACC = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = NACC * BN;
@@ -79,10 +83,22 @@ struct GCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+// Position in a ring of N slots and the parity of its use there.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ void next() {
+    if (++at == N) at = 0, parity ^= 1;
+  }
+};
+
 struct Tile {
   int e, row0, rows;  // expert and its rows
   int l0, c0, ncols;  // first lane of the tile, first column, columns
 };
+
+__host__ __device__ __forceinline__ int tiles_of(int n, int size) { return (n + size - 1) / size; }
 
 // The tiles of the call, experts in order; first[e] = tiles before expert e.
 // Within an expert the column tiles go in groups that share a pass over the lane
@@ -90,17 +106,21 @@ struct Tile {
 template <class G, GroupedMode MODE>
 struct Tiles {
   const int *first, *beg;
-  int E, L, nL, C, e = 0;
+  int E, L, C, e = 0;
+  // lanes and columns of an expert with `rows` rows
+  __device__ int lanes(int rows) const { return G::ROWS ? rows : L; }
+  __device__ int cols(int rows) const { return G::ROWS || MODE == GG_DW ? C : rows; }
+  __device__ int count(int rows) const { return tiles_of(lanes(rows), G::LANES) * tiles_of(cols(rows), G::BN); }
   __device__ bool get(int w, Tile &t) {
     if (w >= first[E]) return false;
     while (w >= first[e + 1]) ++e;
-    const int i = w - first[e], rows = beg[e + 1] - beg[e], total = MODE == GG_DW ? C : rows;
-    const int nc = (total + G::BN - 1) / G::BN;
-    const int grp = i / (kRowTileGroup * nL), rem = i - grp * kRowTileGroup * nL;
+    const int i = w - first[e], rows = beg[e + 1] - beg[e], total = cols(rows);
+    const int nl = tiles_of(lanes(rows), G::LANES), nc = tiles_of(total, G::BN);
+    const int grp = i / (kRowTileGroup * nl), rem = i - grp * kRowTileGroup * nl;
     const int gsz = min(kRowTileGroup, nc - grp * kRowTileGroup);
     const int l = rem / gsz, c = grp * kRowTileGroup + rem % gsz;
-    // equal tiles, rounded to the MMA's step: one short tile would leave its CTAs idle
-    const int step = 16 * G::CG, tc = ((total + nc - 1) / nc + step - 1) / step * step;
+    // equal tiles, rounded to the MMA's step: one short tile would leave its CTAs idle (ROWS: whole scale blocks)
+    const int step = G::ROWS ? G::BN : 16 * G::CG, tc = tiles_of(tiles_of(total, nc), step) * step;
     t.e = e;
     t.row0 = beg[e];
     t.rows = rows;
@@ -114,10 +134,10 @@ struct Tiles {
 // TMEM to registers in the layout of 8 x 8 blocks (16x256b): of 32 lanes x 32
 // columns at taddr, r[h][4 j + 2 g + i] is lane 16 h + 8 g + id / 4, column
 // 8 j + 2 (id % 4) + i for thread id.  A thread so holds two neighbouring columns
-// of four lanes: a column's scale, wanted by every lane, is read from shared
-// memory once for four of them (one lane per thread would be bound by those
-// reads), and the block transposes with one instruction for the stores.
-// The values are there after wait_block of the same r.
+// of four lanes: a column's scale is read from shared memory once for four of
+// them, and the block transposes with one instruction for the stores.  (These
+// loads run at half the rate of 32x32b: 550 against 260 cycles for 128 columns
+// in eight warps.)  The values are there after wait_block of the same r.
 __device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -242,6 +262,53 @@ __device__ __forceinline__ void store_block(const GroupedArgs &P, long long base
   }
 }
 
+// Stores n columns of one output row, N / 2 pairs in registers, to out + base.
+template <int N, int DT>
+__device__ __forceinline__ void store_row_b16(uint16_t *out, int words, int n, const uint64_t (&v)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i += 4) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(low(v[i + j]), high(v[i + j]));
+    if (words == 8) {
+      if (2 * i < n) *reinterpret_cast<uint4 *>(out + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 2 * (i + j);
+        if (words == 2) {
+          if (c < n) *reinterpret_cast<uint32_t *>(out + c) = w[j];
+        } else {
+          if (c < n) out[c] = (uint16_t)w[j];
+          if (c + 1 < n) out[c + 1] = (uint16_t)(w[j] >> 16);
+        }
+      }
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_row(const GroupedArgs &P, long long base, int n, const uint64_t (&v)[N / 2]) {
+  if (P.out_dtype == TILEQ_DT_F32) {
+    float *out = reinterpret_cast<float *>(P.out) + base;
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2) {
+      if (P.store_words == 8) {
+        if (2 * i < n) *reinterpret_cast<float4 *>(out + 2 * i) = make_float4(low(v[i]), high(v[i]), low(v[i + 1]), high(v[i + 1]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (2 * (i + j) < n) out[2 * (i + j)] = low(v[i + j]);
+          if (2 * (i + j) + 1 < n) out[2 * (i + j) + 1] = high(v[i + j]);
+        }
+      }
+    }
+  } else if (P.out_dtype == TILEQ_DT_BF16) {
+    store_row_b16<N, TILEQ_DT_BF16>(reinterpret_cast<uint16_t *>(P.out) + base, P.store_words, n, v);
+  } else {
+    store_row_b16<N, TILEQ_DT_F16>(reinterpret_cast<uint16_t *>(P.out) + base, P.store_words, n, v);
+  }
+}
+
 template <class G, GroupedMode MODE>
 __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_constant__ GroupedArgs P) {
   constexpr int CG = G::CG, SQ = G::SQ, NACC = G::NACC, PARTS = G::PARTS;
@@ -262,6 +329,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   auto stage_a = [&](int s) { return smem + s * G::STAGE; };
   auto stage_b = [&](int s) { return smem + s * G::STAGE + G::A_BYTES; };
 
+  Tiles<G, MODE> tiles{first, beg, P.E, P.L, P.C};
   if (threadIdx.x == 0) {
     for (int s = 0; s < SQ; ++s) {
       mbar_init(&full[s], CG);
@@ -292,7 +360,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       }
       int lo = __shfl_up_sync(0xffffffffu, hi, 1);
       if (lane == 0) lo = top;
-      int sum = e < P.E ? P.nL * (((MODE == GG_DW ? P.C : hi - lo) + G::BN - 1) / G::BN) : 0;
+      int sum = e < P.E ? tiles.count(hi - lo) : 0;
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
@@ -309,10 +377,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Tiles<G, MODE> tiles{first, beg, P.E, P.L, P.nL, P.C};
   auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
-  // columns of one part's MMA
-  auto mma_n = [&](const Tile &t) { return (t.ncols + 16 * CG * PARTS - 1) / (16 * CG * PARTS) * (16 * CG); };
+  // parts of the tile that have columns, and the columns of one part's MMA
+  auto parts = [&](const Tile &t) { return PARTS == 1 || t.ncols <= G::PC ? 1 : 2; };
+  auto mma_n = [&](const Tile &t) { return G::ROWS ? G::PC : tiles_of(t.ncols, 16 * CG) * 16 * CG; };
   Tile t;
   bool ok = true;
 
@@ -321,92 +389,94 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   }
   if (warp == 0) {
     // ============================================================ producer
-    uint32_t qi = 0;
+    Ring<SQ> q;
     for (int w = unit0; ok && tiles.get(w, t); w += units) {
       const int nk = steps(t), half = mma_n(t) / CG;
       const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
-      constexpr int ABOX = MODE == GG_FWD ? 1 : 2;         // boxes of A: 128 rows, or twice 64 columns
-      constexpr int BBOX = MODE == GG_DW ? 64 : G::BOX_ROWS;  // columns of the tile in one box of B
-      const int nbox = PARTS == 2 ? 2 : (half + BBOX - 1) / BBOX;
-      const int bstep = PARTS == 2 ? half * CG : BBOX;  // columns from one box to the next (two parts: a box each)
+      constexpr int ABOX = MODE == GG_FWD ? 1 : 2;           // boxes of A: 128 rows, or twice 64 columns
+      constexpr int BBOX = MODE == GG_DW ? 64 : G::BOX_B;    // columns of the tile in one box of B
+      const int nbox = G::ROWS ? parts(t) : tiles_of(half, BBOX);
       const uint32_t bytes = G::A_BYTES + nbox * BBOX * 128;
-      for (int kb = 0; kb < nk; ++kb, ++qi) {
-        const int s = qi % SQ;
+      // One lane per box (a single lane would need the time of a whole stage to issue five or six copies):
+      // this lane's box and how far it moves from one step to the next
+      const bool is_a = lane < ABOX;
+      const int i = is_a ? lane : lane - ABOX;
+      uint8_t *dst = is_a ? stage_a(0) + i * 8192 : stage_b(0) + i * BBOX * 128;
+      const CUtensorMap *map = is_a ? &P.amap : &P.bmap;
+      int x, y, z = 0;
+      const bool along_x = is_a ? MODE == GG_FWD : MODE != GG_DW;  // is the reduction the inner dimension?
+      if (along_x) {
+        x = 0;
+        // rows of x (dy): from the expert's first one; of w: within the expert (a box per part: 128 apart)
+        y = is_a ? l0 + (G::ROWS ? t.row0 : 0) : c0 + i * (G::ROWS ? G::PC : BBOX) + (G::ROWS ? 0 : t.row0);
+      } else {
+        x = (is_a ? l0 : c0) + i * 64;
+        y = MODE == GG_DW ? t.row0 : 0;
+      }
+      if (MODE != GG_DW && is_a != G::ROWS) z = t.e;
+      for (int kb = 0; kb < nk; ++kb, q.next()) {
         const int left = MODE == GG_DW ? t.rows - kb * G::KE : G::KE;
         const bool cut = left < G::KE && (left & 15);  // the last MMA of the step reaches the next expert's rows
-        if (qi >= (uint32_t)SQ && !(ok = warp_wait(&empty[s], ((qi / SQ) - 1) & 1, P.status))) break;
-        const uint32_t bar = cut ? smem_addr(&tail[s]) : CG == 2 ? tc::map_cta(&full[s], 0) : smem_addr(&full[s]);
+        if (!(ok = warp_wait(&empty[q.at], q.parity ^ 1, P.status))) break;
+        const uint32_t bar = cut ? smem_addr(&tail[q.at]) : CG == 2 ? tc::map_cta(&full[q.at], 0) : smem_addr(&full[q.at]);
         if (lane == 0) {
           if (cut || CG == 1)
-            mbar_arrive_expect_tx(cut ? &tail[s] : &full[s], bytes);
+            mbar_arrive_expect_tx(cut ? &tail[q.at] : &full[q.at], bytes);
           else
             tc::arrive_expect_at(bar, bytes);
         }
-        // one lane per box: a single lane would need the time of a whole stage to issue five or six copies
-        if (lane < ABOX + nbox) {
-          const bool is_a = lane < ABOX;
-          const int i = is_a ? lane : lane - ABOX;
-          uint8_t *dst = is_a ? stage_a(s) + i * 8192 : stage_b(s) + i * BBOX * 128;
-          const CUtensorMap *map = is_a ? &P.amap : &P.bmap;
-          int x, y, z = 0;
-          if (MODE == GG_FWD || (MODE == GG_DX && !is_a)) {
-            x = kb * G::KE;
-            y = is_a ? l0 : t.row0 + c0 + i * bstep;
-          } else {
-            x = (is_a ? l0 : c0) + i * 64;
-            y = (MODE == GG_DW ? t.row0 : 0) + kb * 64;
-          }
-          if (is_a && MODE != GG_DW) z = t.e;
-          tc::tma_3d<CG>(dst, map, x, y, z, bar);
-        }
+        if (lane < ABOX + nbox) tc::tma_3d<CG>(dst + q.at * G::STAGE, map, x, y, z, bar);
+        x += along_x ? G::KE : 0;
+        y += along_x ? 0 : G::KE;
       }
     }
     // no copy of this CTA may land and no commit may arrive after it has gone
-    if (lane == 0)
-      for (uint32_t i = qi > (uint32_t)SQ ? qi - SQ : 0; ok && i < qi; ++i)
-        ok = mbar_wait(&empty[i % SQ], (i / SQ) & 1, P.status);
-    if (lane == 0 && !ok && rank == 0)
-      for (uint32_t i = qi > (uint32_t)SQ ? qi - SQ : 0; i < qi; ++i) mbar_wait(&full[i % SQ], (i / SQ) & 1, P.status);
+    if (lane == 0) {
+      for (int i = 0; ok && i < SQ; ++i, q.next()) ok = mbar_wait(&empty[q.at], q.parity ^ 1, P.status);
+      if (!ok && rank == 0)
+        for (int i = 0; i < SQ; ++i, q.next()) mbar_wait(&full[q.at], q.parity ^ 1, P.status);
+    }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     if (rank == 0) {
       constexpr bool A_MN = MODE != GG_FWD, B_MN = MODE == GG_DW;  // output dimension contiguous
       const uint32_t fmt = P.bf16 && !G::F8 ? (1u << 7) | (1u << 10) : 0u;
-      uint32_t qi = 0, ai = 0;
+      Ring<SQ> q;
+      Ring<NACC> acc[PARTS];
+      const uint64_t ad0 = tc::sdesc(smem_addr(stage_a(0)), A_MN ? 8192 : 16);
+      const uint64_t bd0 = tc::sdesc(smem_addr(stage_b(0)), B_MN ? 8192 : 16);
       for (int w = unit0; ok && tiles.get(w, t); w += units) {
-        const int nk = steps(t);
+        const int nk = steps(t), np = parts(t);
         if (nk == 0) continue;
         const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                                ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
-        for (int kb = 0; kb < nk; ++kb, ++qi) {
-          const int s = qi % SQ, ab = ai % NACC;
+        for (int kb = 0; kb < nk; ++kb, q.next()) {
           const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
-          if (!(ok = warp_wait(&full[s], (qi / SQ) & 1, P.status, cut))) break;
+          const bool last = G::F8 || kb == nk - 1, first_k = G::F8 || kb == 0;
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
-          const uint64_t ad = tc::sdesc(smem_addr(stage_a(s)), A_MN ? 8192 : 16);
-          const uint64_t bd = tc::sdesc(smem_addr(stage_b(s)), B_MN ? 8192 : 16);
+          const uint64_t at = (uint64_t)(q.at * (G::STAGE >> 4));
+          if (!(ok = warp_wait(&full[q.at], q.parity, P.status, cut))) break;
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
-            const int pa = part * NACC + ab;
-            if ((G::F8 || kb == 0) && ai >= (uint32_t)NACC &&
-                !(ok = warp_wait(&acc_empty[pa], ((ai / NACC) - 1) & 1, P.status)))
-              break;
+            if (part >= np) break;
+            const int pa = part * NACC + acc[part].at;
+            if (first_k && !(ok = warp_wait(&acc_empty[pa], acc[part].parity ^ 1, P.status))) break;
             tc::fence_after();
             if (tc::elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 if (MODE != GG_DW || kk < nmma)
-                  tc::mma_ss<CG, G::F8>(tmem + pa * G::PC, ad + (uint64_t)(kk * (A_MN ? 128 : 2)),
-                                        bd + (uint64_t)(kk * (B_MN ? 128 : 2) + part * (8192 >> 4)), idesc,
-                                        (kk || (!G::F8 && kb)) ? 1u : 0u);
-              if (part == PARTS - 1) tc::commit_cg<CG>(&empty[s]);
-              if (G::F8 || kb == nk - 1) tc::commit_cg<CG>(&acc_full[pa]);
+                  tc::mma_ss<CG, G::F8>(tmem + pa * G::PC, ad0 + at + (uint64_t)(kk * (A_MN ? 128 : 2)),
+                                        bd0 + at + (uint64_t)(kk * (B_MN ? 128 : 2) + part * (8192 >> 4)), idesc,
+                                        (kk || !first_k) ? 1u : 0u);
+              if (part == np - 1) tc::commit_cg<CG>(&empty[q.at]);
+              if (last) tc::commit_cg<CG>(&acc_full[pa]);
             }
             __syncwarp();
+            if (last) acc[part].next();
           }
           if (!ok) break;
-          if (G::F8 || kb == nk - 1) ++ai;
         }
       }
       // all issued MMAs have retired before tensor memory is released
@@ -443,110 +513,156 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     if constexpr (G::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsEpilogue));
     const int half = (warp - kFirstEpw) >> 2;
     const uint32_t lane_addr = tc::lane_base(warp);  // TMEM lane quadrant of this warp
-    uint32_t ai = 0, gi = 0;
-    // (fp8: the four warps of a named barrier stay together, also after a wait that gave up)
+    const int part = PARTS == 2 ? half : 0;
+    uint64_t *my_full = acc_full + part * NACC, *my_empty = acc_empty + part * NACC;
+    Ring<NACC> acc;
+    uint32_t group = 0;
+    auto release = [&] {  // this warp has read the accumulator
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&my_empty[acc.at], 0));
+      acc.next();
+    };
+    // (narrow fp8: the four warps of a named barrier stay together, also after a wait that gave up)
     for (int w = unit0; (ok || G::F8) && tiles.get(w, t); w += units) {
       const int nk = steps(t), l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
-      const int cw = half * (PARTS == 2 ? mma_n(t) : G::COLS);              // first column of this warp
-      const int mine = min(t.ncols - cw, PARTS == 2 ? mma_n(t) : G::COLS);  // its columns, none if <= 0
-      const int nl = P.L - l0;
-      const long long base = (MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)(t.c0 + cw) * P.ldo
-                                            : (long long)(t.row0 + t.c0 + cw) * P.ldo) + l0;
-      if constexpr (!G::F8) {
-        const int ab = ai % NACC;
-        if (nk > 0) {
-          if (!(ok = warp_wait(&acc_full[ab], (ai / NACC) & 1, P.status))) break;
-          tc::fence_after();
-        }
-#pragma unroll 1
-        for (int c = 0; c < mine; c += 32) {
-          uint32_t r[2][16];
-          if (nk > 0) {
-            ld_block(tmem + lane_addr + ab * G::BN + cw + c, r);
-            wait_block(r);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint64_t v[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
-              v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
-            store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
-          }
-        }
-        if (nk > 0) {
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[ab], 0));
-          ++ai;
-        }
-      } else {
-        constexpr int CH = G::CHUNK, NCH = G::COLS / CH, GROUPS = CH / 8;
-        uint64_t acc[G::COLS / 8][4];  // [8 columns][lane block]: two columns, folded by one packed FMA
-#pragma unroll
-        for (int i = 0; i < G::COLS / 8; ++i)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) acc[i][g] = 0;
-        const int part = PARTS == 2 ? half : 0, col0 = PARTS == 2 ? 0 : cw;
-        // scales of kScaleGroup blocks at a time: thread tid's column (the last one where it has none) and block,
-        // fetched while the group before is folded
-        const int tid = threadIdx.x & 127;  // within the four warps that share these columns
-        const float *xs = P.xs + t.row0 + t.c0 + (mine > 0 ? cw + min(tid, mine - 1) : 0);
-        const float *ws = P.ws + ((long long)t.e * P.nLb + min((t.l0 + (int)rank * 128) / 128, P.nLb - 1)) * P.nKb;
-        float sx[kScaleGroup], sw[kScaleGroup];
+      const int cw = half * G::COLS;                  // first column of this warp
+      const int mine = min(t.ncols - cw, G::COLS);    // its columns, none if <= 0
+      if constexpr (G::ROWS) {
+        if (mine <= 0) continue;  // a part without columns has no MMAs either
+        // this thread's row of x and y, and its scale with the part's weight scale: fetched two blocks ahead
+        const int row = min(l0 + lane, t.rows - 1);
+        const float *xs = P.xs + t.row0 + row;
+        const float *ws = P.ws + ((long long)t.e * P.nOb + t.c0 / 128 + part) * P.nKb;
+        float sx[2], sw[2];
         auto fetch = [&](int kb) {
 #pragma unroll
-          for (int j = 0; j < kScaleGroup; ++j) {
+          for (int j = 0; j < 2; ++j) {
             const int k = min(kb + j, nk - 1);
             sx[j] = __ldg(xs + k * P.ld_xs);
             sw[j] = __ldg(ws + k);
           }
         };
+        uint64_t v[G::COLS / 2];  // pairs of neighbouring columns: one packed FMA folds both
+#pragma unroll
+        for (int i = 0; i < G::COLS / 2; ++i) v[i] = 0;
         fetch(0);
 #pragma unroll 1
-        for (int kg = 0; kg < nk; kg += kScaleGroup) {
-          float *sc = scale + (gi++ & 1) * kScaleGroup * G::BN + half * G::COLS;
-          if (G::COLS == 128 || tid < G::COLS) {
+        for (int kg = 0; kg < nk; kg += 2) {
+          float s[2];
 #pragma unroll
-            for (int j = 0; j < kScaleGroup; ++j) sc[j * G::BN + tid] = sx[j] * sw[j];
+          for (int j = 0; j < 2; ++j) s[j] = sx[j] * sw[j];
+          fetch(kg + 2);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (kg + j < nk) {
+              const uint64_t ss = pair(__float_as_uint(s[j]), __float_as_uint(s[j]));
+              ok = ok && warp_wait(&my_full[acc.at], acc.parity, P.status);
+              tc::fence_after();
+              const uint32_t ta = tmem + lane_addr + (part * NACC + acc.at) * G::PC;
+              uint32_t r[2][16];
+              tc::ld16_nowait(ta, r[0]);
+#pragma unroll
+              for (int c = 0; c < G::COLS / 16; ++c) {
+                tc::wait_ld();
+                tie(r[c & 1]);
+                if (c + 1 < G::COLS / 16)
+                  tc::ld16_nowait(ta + 16 * (c + 1), r[(c + 1) & 1]);
+                else
+                  release();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) fma2(v[8 * c + i], pair(r[c & 1][2 * i], r[c & 1][2 * i + 1]), ss);
+              }
+            }
           }
-          fetch(kg + kScaleGroup);
-          // also keeps these warps within one group of each other: two buffers of scales do
-          named_sync(1 + half, 128);
-          sc += 2 * (lane & 3);
-#pragma unroll 1
-          for (int kb = kg; kb < min(kg + kScaleGroup, nk); ++kb, ++ai, sc += G::BN) {
-            const int pa = part * NACC + ai % NACC;
-            ok = ok && warp_wait(&acc_full[pa], (ai / NACC) & 1, P.status);
+        }
+        if (ok && l0 + lane < t.rows)
+          store_row<G::COLS>(P, (long long)(t.row0 + l0 + lane) * P.ldo + t.c0 + cw, mine, v);
+      } else {
+        const int nl = P.L - l0;
+        const long long base = (MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)(t.c0 + cw) * P.ldo
+                                              : (long long)(t.row0 + t.c0 + cw) * P.ldo) + l0;
+        if constexpr (!G::F8) {
+          if (nk > 0) {
+            if (!(ok = warp_wait(&my_full[acc.at], acc.parity, P.status))) break;
             tc::fence_after();
-            const uint32_t ta = tmem + lane_addr + pa * G::PC + col0;
-            uint32_t r[2][2][CH / 2];
-            if (mine > 0) {
+          }
+#pragma unroll 1
+          for (int c = 0; c < mine; c += 32) {
+            uint32_t r[2][16];
+            if (nk > 0) {
+              ld_block(tmem + lane_addr + acc.at * G::BN + cw + c, r);
+              wait_block(r);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint64_t v[4];
+#pragma unroll
+              for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
+                v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
+              store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
+            }
+          }
+          if (nk > 0) release();
+        } else {
+          uint64_t v[G::COLS / 8][4];  // [8 columns][lane block]: two columns, folded by one packed FMA
+#pragma unroll
+          for (int i = 0; i < G::COLS / 8; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[i][g] = 0;
+          // Scales of kScaleGroup blocks at a time, fetched while the group before is folded: thread tid has column
+          // tid % 64 (the last one where there are fewer) of every other block.
+          static_assert(G::F8 && G::COLS <= 64, "128 threads stage two blocks at a time");
+          const int tid = threadIdx.x & 127, col = tid & 63, odd = tid >> 6;
+          const float *xs = P.xs + t.row0 + t.c0 + min(col, mine - 1);
+          const float *ws = P.ws + ((long long)t.e * P.nOb + min((t.l0 + (int)rank * 128) / 128, P.nOb - 1)) * P.nKb;
+          float sx[kScaleGroup / 2], sw[kScaleGroup / 2];
+          auto fetch = [&](int kb) {
+#pragma unroll
+            for (int j = 0; j < kScaleGroup / 2; ++j) {
+              const int k = min(kb + 2 * j + odd, nk - 1);
+              sx[j] = __ldg(xs + k * P.ld_xs);
+              sw[j] = __ldg(ws + k);
+            }
+          };
+          fetch(0);
+#pragma unroll 1
+          for (int kg = 0; kg < nk; kg += kScaleGroup) {
+            float *sc = scale + (group++ & 1) * kScaleGroup * G::BN;
+#pragma unroll
+            for (int j = 0; j < kScaleGroup / 2; ++j) sc[(2 * j + odd) * G::BN + col] = sx[j] * sw[j];
+            fetch(kg + kScaleGroup);
+            // also keeps these warps within one group of each other: two buffers of scales do
+            named_sync(1, 128);
+            sc += 2 * (lane & 3);
+#pragma unroll 1
+            for (int kb = kg; kb < min(kg + kScaleGroup, nk); ++kb, sc += G::BN) {
+              ok = ok && warp_wait(&my_full[acc.at], acc.parity, P.status);
+              tc::fence_after();
+              const uint32_t ta = tmem + lane_addr + acc.at * G::BN;
+              uint32_t r[2][2][8];
               ld_block(ta, r[0]);
 #pragma unroll
-              for (int ch = 0; ch < NCH; ++ch) {
-                if (ch * CH < mine) {
-                  wait_block(r[ch & 1]);
-                  if (ch + 1 < NCH && (ch + 1) * CH < mine) ld_block(ta + (ch + 1) * CH, r[(ch + 1) & 1]);
+              for (int c = 0; c < G::COLS / 16; ++c) {
+                if (16 * c < mine) {
+                  wait_block(r[c & 1]);
+                  if (c + 1 < G::COLS / 16 && 16 * (c + 1) < mine) ld_block(ta + 16 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                  for (int j = 0; j < GROUPS; ++j) {
-                    const uint64_t s = *reinterpret_cast<const uint64_t *>(sc + ch * CH + 8 * j);
+                  for (int j = 0; j < 2; ++j) {
+                    const uint64_t s = *reinterpret_cast<const uint64_t *>(sc + 16 * c + 8 * j);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                      fma2(acc[ch * GROUPS + j][g],
-                           pair(r[ch & 1][g >> 1][4 * j + 2 * (g & 1)], r[ch & 1][g >> 1][4 * j + 2 * (g & 1) + 1]), s);
+                      fma2(v[2 * c + j][g], pair(r[c & 1][g >> 1][4 * j + 2 * (g & 1)], r[c & 1][g >> 1][4 * j + 2 * (g & 1) + 1]), s);
                   }
                 }
               }
+              release();
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&acc_empty[pa], 0));
           }
-        }
 #pragma unroll
-        for (int j = 0; j < G::COLS / 8; ++j)
-          if (ok && 8 * j < mine) store_block(P, base + 8 * j * P.ldo, mine - 8 * j, nl, lane, acc[j]);
+          for (int j = 0; j < G::COLS / 8; ++j)
+            if (ok && 8 * j < mine) store_block(P, base + 8 * j * P.ldo, mine - 8 * j, nl, lane, v[j]);
+        }
       }
     }
   }
@@ -613,7 +729,7 @@ cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
 }  // namespace
 
 int grouped_tile_cols(GroupedKernel k) { return k == GG_WIDE ? Wide::BN : Narrow::BN; }
-int grouped_box_rows(GroupedKernel k) { return k == GG_WIDE ? Wide::BOX_ROWS : Narrow::BOX_ROWS; }
+int grouped_box_rows(GroupedKernel k) { return k == GG_WIDE ? Wide::BOX_B : Narrow::BOX_B; }
 int grouped_tile_lanes(GroupedKernel k) { return k == GG_WIDE ? Wide::LANES : Narrow::LANES; }
 
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,

@@ -16,24 +16,23 @@ enum GroupedMode { GG_FWD = 0, GG_DX = 1, GG_DW = 2 };
 
 struct GroupedArgs {
   // a: the operand of the output's contiguous dimension (128 TMEM lanes per
-  // CTA), b: that of the output's rows (TMEM columns)
+  // CTA), b: that of the output's rows (TMEM columns); wide fp8: exchanged
   alignas(64) CUtensorMap amap;
   alignas(64) CUtensorMap bmap;
   const int32_t *offsets;  // device [E + 1], or null: one expert with all P rows
   int E, P;
-  int L;                   // contiguous output dimension
-  int C;                   // GG_DW: output rows per expert
+  int L;                   // contiguous output dimension (wide fp8: not used)
+  int C;                   // GG_DW: output rows per expert; wide fp8: the contiguous output dimension
   int R;                   // GG_FWD, GG_DX: reduction length
-  int nL;                  // lane tiles
   int bf16;                // 16-bit operands: 1 bf16, 0 fp16
   void *out;
   int out_dtype;           // TILEQ_DT_*
   int store_words;         // 16-bit results that one store may take: 1, 2 or 8 neighbours
   long long ldo, out_stride;
-  const float *xs;         // fp8: scales of the rows [R / 128][ld_xs], of the weights [E][nLb][nKb]
+  const float *xs;         // fp8: scales of the rows [nKb][ld_xs], of the weights [E][nOb][nKb]
   const float *ws;
   long long ld_xs;
-  int nLb, nKb;
+  int nOb, nKb;
   int *status;
 };
 
