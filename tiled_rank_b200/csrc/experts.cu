@@ -112,8 +112,9 @@ GroupedKernel pick(GroupedMode mode, const tileq_grouped *g, bool fp8) {
 tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const Operand &weights, const Operand &rows,
                  int contig, bool fp8, cudaStream_t stream) {
   const GroupedKernel k = pick(mode, g, fp8);
-  const bool on_lanes = fp8 && k == GG_WIDE;
-  const int bn = grouped_tile_cols(k), lanes = grouped_tile_lanes(k), cg = lanes / 128;
+  const GroupedTile t = grouped_tile(k, fp8);
+  const bool on_lanes = t.rows_on_lanes;
+  const int cg = t.lanes / 128;
   a.offsets = g->expert_offsets;
   a.E = g->E;
   a.P = g->P;
@@ -122,12 +123,14 @@ tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const
   a.bf16 = g->dtype == TILEQ_DT_BF16;
   a.out_dtype = g->out_dtype;
   const auto all = [&](long long n) { return contig % n == 0 && a.ldo % n == 0 && a.out_stride % n == 0; };
-  a.store_words = all(8) ? 8 : all(2) ? 2 : 1;  // out is 16-byte aligned
-  const long long row_tiles = g->P / (on_lanes ? lanes : bn) + std::min(g->E, g->P);  // at most
-  const long long tiles = div_up(contig, on_lanes ? bn : lanes) * (mode == GG_DW ? g->E * div_up(a.C, bn) : row_tiles);
+  // out is 16-byte aligned; the 32-byte stores of 16 bf16 or 8 fp32 want more
+  const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  a.store_words = wide && all(16) ? 16 : all(8) && (wide || g->out_dtype != TILEQ_DT_F32) ? 8 : all(2) ? 2 : 1;
+  const long long row_tiles = g->P / (on_lanes ? t.lanes : t.cols) + std::min(g->E, g->P);  // at most
+  const long long tiles = div_up(contig, on_lanes ? t.cols : t.lanes) * (mode == GG_DW ? g->E * div_up(a.C, t.cols) : row_tiles);
   if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
   if (!encode(&a.amap, on_lanes ? rows : weights, mode == GG_FWD ? 128 : 64) ||
-      !encode(&a.bmap, on_lanes ? weights : rows, mode == GG_DW ? 64 : grouped_box_rows(k)))
+      !encode(&a.bmap, on_lanes ? weights : rows, mode == GG_DW ? 64 : t.box_b))
     return TILEQ_ERR_CUDA;
   const int sms = sm_count();
   if (sms < cg) return TILEQ_ERR_CUDA;

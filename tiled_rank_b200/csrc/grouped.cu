@@ -58,7 +58,6 @@ struct GCfg {
   static constexpr bool ROWS = F8 && BN == 256;  // the experts' rows on the lanes, d_out on the columns
   static constexpr int LANES = 128 * CG;
   static constexpr int KE = F8 ? 128 : 64;  // reduction elements per stage (128 bytes)
-  static constexpr int BOX_B = BN == 256 ? 64 : 32;  // rows of one box of B where the reduction is contiguous
   static constexpr int EPW = BN == 256 ? 8 : 4;
   static constexpr int COLS = BN / (EPW / 4);  // columns of one epilogue warp
   static constexpr int THREADS = (kFirstEpw + EPW) * 32;
@@ -73,6 +72,7 @@ struct GCfg {
   // accumulators of their own, folded by four epilogue warps each: while one part is folded the other's MMAs run
   static constexpr int PARTS = ROWS ? 2 : 1;
   static constexpr int PC = BN / PARTS;  // columns of a part
+  static constexpr int BOX_B = ROWS ? PC / CG : BN == 256 ? 64 : 32;  // rows of a box of B where the reduction is contiguous
   static constexpr int NACC = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = NACC * BN;
   static constexpr int BAR_OFF = SQ * STAGE;
@@ -130,6 +130,13 @@ struct Tiles {
     return true;
   }
 };
+
+// Two barriers asked at once (a single question takes about 100 cycles, also when the answer is yes), then waited for.
+__device__ __forceinline__ bool warp_wait2(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, int *status) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  if (__all_sync(0xffffffffu, ra && rb)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(a, pa, status) && mbar_wait(b, pb, status));
+}
 
 // TMEM to registers in the layout of 8 x 8 blocks (16x256b): of 32 lanes x 32
 // columns at taddr, r[h][4 j + 2 g + i] is lane 16 h + 8 g + id / 4, column
@@ -239,7 +246,7 @@ __device__ __forceinline__ void store_b16(uint16_t *out, long long ldo, int n, i
 template <int DT>
 __device__ __forceinline__ void store_b16(const GroupedArgs &P, long long base, int n, int nl, int id, const uint64_t (&v)[4]) {
   uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base;
-  if (P.store_words == 8)
+  if (P.store_words >= 8)
     store_b16<DT, 8>(out, P.ldo, n, nl, id, v);
   else if (P.store_words == 2)
     store_b16<DT, 2>(out, P.ldo, n, nl, id, v);
@@ -262,20 +269,29 @@ __device__ __forceinline__ void store_block(const GroupedArgs &P, long long base
   }
 }
 
-// Stores n columns of one output row, N / 2 pairs in registers, to out + base.
+// Stores n columns of one output row, N / 2 pairs in registers, to out + base.  A thread has a row of its own, so a
+// store should fill whole 32-byte sectors where the row allows it (WORDS == 16).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 template <int N, int DT>
 __device__ __forceinline__ void store_row_b16(uint16_t *out, int words, int n, const uint64_t (&v)[N / 2]) {
 #pragma unroll
-  for (int i = 0; i < N / 2; i += 4) {
-    uint32_t w[4];
+  for (int i = 0; i < N; i += 16) {
+    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(low(v[i + j]), high(v[i + j]));
-    if (words == 8) {
-      if (2 * i < n) *reinterpret_cast<uint4 *>(out + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 8; ++j) w[j] = pack2<DT>(low(v[i / 2 + j]), high(v[i / 2 + j]));
+    if (words == 16) {
+      if (i < n) store32(out + i, w);
+    } else if (words == 8) {
+      if (i < n) *reinterpret_cast<uint4 *>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (i + 8 < n) *reinterpret_cast<uint4 *>(out + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 2 * (i + j);
+      for (int j = 0; j < 8; ++j) {
+        const int c = i + 2 * j;
         if (words == 2) {
           if (c < n) *reinterpret_cast<uint32_t *>(out + c) = w[j];
         } else {
@@ -291,15 +307,16 @@ __device__ __forceinline__ void store_row(const GroupedArgs &P, long long base, 
   if (P.out_dtype == TILEQ_DT_F32) {
     float *out = reinterpret_cast<float *>(P.out) + base;
 #pragma unroll
-    for (int i = 0; i < N / 2; i += 2) {
-      if (P.store_words == 8) {
-        if (2 * i < n) *reinterpret_cast<float4 *>(out + 2 * i) = make_float4(low(v[i]), high(v[i]), low(v[i + 1]), high(v[i + 1]));
+    for (int i = 0; i < N; i += 8) {
+      if (P.store_words >= 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = (uint32_t)(v[i / 2 + j / 2] >> (j & 1 ? 32 : 0));
+        if (i < n) store32(out + i, w);
       } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (2 * (i + j) < n) out[2 * (i + j)] = low(v[i + j]);
-          if (2 * (i + j) + 1 < n) out[2 * (i + j) + 1] = high(v[i + j]);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (i + j < n) out[i + j] = __uint_as_float((uint32_t)(v[i / 2 + j / 2] >> (j & 1 ? 32 : 0)));
       }
     }
   } else if (P.out_dtype == TILEQ_DT_BF16) {
@@ -333,14 +350,14 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   if (threadIdx.x == 0) {
     for (int s = 0; s < SQ; ++s) {
       mbar_init(&full[s], CG);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], PARTS);
       mbar_init(&tail[s], 1);
     }
     for (int b = 0; b < PARTS * NACC; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], G::EPW / PARTS * CG);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, PARTS);
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc_cg<CG>(tmem_slot, G::TMEM_COLS);
@@ -436,47 +453,50 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       if (!ok && rank == 0)
         for (int i = 0; i < SQ; ++i, q.next()) mbar_wait(&full[q.at], q.parity ^ 1, P.status);
     }
-  } else if (warp == 1) {
-    // ============================================================ MMA issuer
+  } else if (warp == 1 || (PARTS == 2 && warp == 2)) {
+    // ============================================================ MMA issuer (one for each part)
+    // A stage costs a warp some 100 cycles for each barrier it asks and 200 to issue: with two accumulators a
+    // stage one warp would not keep the tensor core busy.
     if (rank == 0) {
       constexpr bool A_MN = MODE != GG_FWD, B_MN = MODE == GG_DW;  // output dimension contiguous
       const uint32_t fmt = P.bf16 && !G::F8 ? (1u << 7) | (1u << 10) : 0u;
+      const int part = PARTS == 2 ? warp - 1 : 0;
       Ring<SQ> q;
-      Ring<NACC> acc[PARTS];
+      Ring<NACC> acc;
       const uint64_t ad0 = tc::sdesc(smem_addr(stage_a(0)), A_MN ? 8192 : 16);
-      const uint64_t bd0 = tc::sdesc(smem_addr(stage_b(0)), B_MN ? 8192 : 16);
+      const uint64_t bd0 = tc::sdesc(smem_addr(stage_b(0)) + part * (G::PC / CG * 128), B_MN ? 8192 : 16);
       for (int w = unit0; ok && tiles.get(w, t); w += units) {
-        const int nk = steps(t), np = parts(t);
-        if (nk == 0) continue;
+        const int nk = steps(t);
+        const bool mine = part < parts(t);
         const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                                ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
         for (int kb = 0; kb < nk; ++kb, q.next()) {
           const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
           const bool last = G::F8 || kb == nk - 1, first_k = G::F8 || kb == 0;
+          const int pa = part * NACC + acc.at;
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
           const uint64_t at = (uint64_t)(q.at * (G::STAGE >> 4));
-          if (!(ok = warp_wait(&full[q.at], q.parity, P.status, cut))) break;
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            if (part >= np) break;
-            const int pa = part * NACC + acc[part].at;
-            if (first_k && !(ok = warp_wait(&acc_empty[pa], acc[part].parity ^ 1, P.status))) break;
-            tc::fence_after();
-            if (tc::elect_one()) {
+          if (mine && first_k && !cut)
+            ok = warp_wait2(&full[q.at], q.parity, &acc_empty[pa], acc.parity ^ 1, P.status);
+          else
+            ok = warp_wait(&full[q.at], q.parity, P.status, cut) &&
+                 (!(mine && first_k) || warp_wait(&acc_empty[pa], acc.parity ^ 1, P.status));
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect_one()) {
+            if (mine) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 if (MODE != GG_DW || kk < nmma)
                   tc::mma_ss<CG, G::F8>(tmem + pa * G::PC, ad0 + at + (uint64_t)(kk * (A_MN ? 128 : 2)),
-                                        bd0 + at + (uint64_t)(kk * (B_MN ? 128 : 2) + part * (8192 >> 4)), idesc,
-                                        (kk || !first_k) ? 1u : 0u);
-              if (part == np - 1) tc::commit_cg<CG>(&empty[q.at]);
+                                        bd0 + at + (uint64_t)(kk * (B_MN ? 128 : 2)), idesc, (kk || !first_k) ? 1u : 0u);
               if (last) tc::commit_cg<CG>(&acc_full[pa]);
             }
-            __syncwarp();
-            if (last) acc[part].next();
+            tc::commit_cg<CG>(&empty[q.at]);
           }
-          if (!ok) break;
+          __syncwarp();
+          if (mine && last) acc.next();
         }
       }
       // all issued MMAs have retired before tensor memory is released
@@ -517,10 +537,11 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     uint64_t *my_full = acc_full + part * NACC, *my_empty = acc_empty + part * NACC;
     Ring<NACC> acc;
     uint32_t group = 0;
-    auto release = [&] {  // this warp has read the accumulator
+    bool ready = false;
+    const uint32_t release_at = tc::map_cta(my_empty, 0);
+    auto release = [&] {  // this warp has read the accumulator (wait::ld is the whole warp's)
       tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive_relaxed_at(tc::map_cta(&my_empty[acc.at], 0));
+      if (lane == 0) tc::arrive_relaxed_at(release_at + acc.at * 8);
       acc.next();
     };
     // (narrow fp8: the four warps of a named barrier stay together, also after a wait that gave up)
@@ -530,7 +551,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       const int mine = min(t.ncols - cw, G::COLS);    // its columns, none if <= 0
       if constexpr (G::ROWS) {
         if (mine <= 0) continue;  // a part without columns has no MMAs either
-        // this thread's row of x and y, and its scale with the part's weight scale: fetched two blocks ahead
+        // this thread's row of x and y, and its scale with the part's weight scale, fetched two blocks ahead
         const int row = min(l0 + lane, t.rows - 1);
         const float *xs = P.xs + t.row0 + row;
         const float *ws = P.ws + ((long long)t.e * P.nOb + t.c0 / 128 + part) * P.nKb;
@@ -538,9 +559,12 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         auto fetch = [&](int kb) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int k = min(kb + j, nk - 1);
-            sx[j] = __ldg(xs + k * P.ld_xs);
-            sw[j] = __ldg(ws + k);
+            if (kb + j < nk) {
+              sx[j] = __ldg(xs);
+              sw[j] = __ldg(ws);
+              xs += P.ld_xs;
+              ++ws;
+            }
           }
         };
         uint64_t v[G::COLS / 2];  // pairs of neighbouring columns: one packed FMA folds both
@@ -548,32 +572,34 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         for (int i = 0; i < G::COLS / 2; ++i) v[i] = 0;
         fetch(0);
 #pragma unroll 1
-        for (int kg = 0; kg < nk; kg += 2) {
-          float s[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) s[j] = sx[j] * sw[j];
-          fetch(kg + 2);
+        for (int kb = 0; kb < nk; kb += 2) {
+          const float s0 = sx[0] * sw[0], s1 = sx[1] * sw[1];
+          fetch(kb + 2);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (kg + j < nk) {
-              const uint64_t ss = pair(__float_as_uint(s[j]), __float_as_uint(s[j]));
-              ok = ok && warp_wait(&my_full[acc.at], acc.parity, P.status);
-              tc::fence_after();
-              const uint32_t ta = tmem + lane_addr + (part * NACC + acc.at) * G::PC;
-              uint32_t r[2][16];
-              tc::ld16_nowait(ta, r[0]);
+            if (kb + j >= nk) break;
+            const uint64_t ss = pair(__float_as_uint(j ? s1 : s0), __float_as_uint(j ? s1 : s0));
+            ok = ok && (ready || warp_wait(&my_full[acc.at], acc.parity, P.status));
+            tc::fence_after();
+            const uint32_t ta = tmem + lane_addr + (part * NACC + acc.at) * G::PC;
+            // 16 columns at a time: with 32 the registers do not suffice for a load beside the FMAs of the one before
+            uint32_t r[2][16];
+            tc::ld16_nowait(ta, r[0]);
 #pragma unroll
-              for (int c = 0; c < G::COLS / 16; ++c) {
-                tc::wait_ld();
-                tie(r[c & 1]);
-                if (c + 1 < G::COLS / 16)
-                  tc::ld16_nowait(ta + 16 * (c + 1), r[(c + 1) & 1]);
-                else
-                  release();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) fma2(v[8 * c + i], pair(r[c & 1][2 * i], r[c & 1][2 * i + 1]), ss);
+            for (int c = 0; c < G::COLS / 16; ++c) {
+              tc::wait_ld();
+              tie(r[c & 1]);
+              if (c + 1 < G::COLS / 16) {
+                tc::ld16_nowait(ta + 16 * (c + 1), r[(c + 1) & 1]);
+              } else {
+                release();
+                // the next block's barrier is asked before the last FMAs, which take as long as the answer
+                ready = mbar_try_wait(&my_full[acc.at], acc.parity);
               }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) fma2(v[8 * c + i], pair(r[c & 1][2 * i], r[c & 1][2 * i + 1]), ss);
             }
+            ready = __all_sync(0xffffffffu, ready);
           }
         }
         if (ok && l0 + lane < t.rows)
@@ -685,7 +711,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
 using Narrow = GCfg<1, 64, false>;
 using NarrowF8 = GCfg<1, 64, true>;
 using Wide = GCfg<2, 256, false>;
-using WideF8 = GCfg<2, 256, true>;
+using WideF8 = GCfg<1, 256, true>;
 
 template <class G, GroupedMode MODE>
 cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
@@ -728,9 +754,11 @@ cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-int grouped_tile_cols(GroupedKernel k) { return k == GG_WIDE ? Wide::BN : Narrow::BN; }
-int grouped_box_rows(GroupedKernel k) { return k == GG_WIDE ? Wide::BOX_B : Narrow::BOX_B; }
-int grouped_tile_lanes(GroupedKernel k) { return k == GG_WIDE ? Wide::LANES : Narrow::LANES; }
+GroupedTile grouped_tile(GroupedKernel k, bool fp8) {
+  if (k == GG_NARROW) return {Narrow::LANES, Narrow::BN, Narrow::BOX_B, false};
+  return fp8 ? GroupedTile{WideF8::LANES, WideF8::BN, WideF8::BOX_B, true} : GroupedTile{Wide::LANES, Wide::BN, Wide::BOX_B, false};
+}
+
 
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream) {

@@ -27,7 +27,8 @@ struct GroupedArgs {
   int bf16;                // 16-bit operands: 1 bf16, 0 fp16
   void *out;
   int out_dtype;           // TILEQ_DT_*
-  int store_words;         // 16-bit results that one store may take: 1, 2 or 8 neighbours
+  int store_words;         // 16-bit results that one store may take: 1, 2, 8 or 16 neighbours
+                           // (fp32: 8 or 16 allow 32-byte stores)
   long long ldo, out_stride;
   const float *xs;         // fp8: scales of the rows [nKb][ld_xs], of the weights [E][nOb][nKb]
   const float *ws;
@@ -37,10 +38,13 @@ struct GroupedArgs {
 };
 
 enum GroupedKernel { GG_NARROW = 0, GG_WIDE = 1 };
-// Rows of the output (TMEM columns) and lanes per tile of each kernel.
-int grouped_tile_cols(GroupedKernel k);
-int grouped_tile_lanes(GroupedKernel k);
-int grouped_box_rows(GroupedKernel k);  // of the row operand's tensor map
+// Tile of a kernel: TMEM lanes (of the pair, where CTAs work in pairs) and columns, rows of a box of the b operand
+// where the reduction is its inner dimension, and whether the experts' rows are on the lanes.
+struct GroupedTile {
+  int lanes, cols, box_b;
+  bool rows_on_lanes;
+};
+GroupedTile grouped_tile(GroupedKernel k, bool fp8);
 // fp8 != 0: e4m3 operands with block scales (GG_FWD only).
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream);
