@@ -32,14 +32,17 @@ ValueError before anything is launched.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _lib as L
 
 _CODE = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16, torch.float32: L.TILEQ_DT_F32}
+_OPERAND = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16}
+_F8 = torch.float8_e4m3fn
 _status_words: dict = {}
+
+# A small product takes the GPU a few microseconds, so what a call costs on the host counts: the checks below read each
+# attribute once and build a message only when they raise.
 
 
 def _status_word(device: torch.device) -> torch.Tensor:
@@ -64,164 +67,175 @@ def expert_status(device="cuda") -> int:
         return L.tileq_device_status(_status_word(device))
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _on_stream(device: torch.device, stream, call):
+    """call(raw stream) with `device` current, on `stream` or its current one; new outputs belong to that stream."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _rows(t: torch.Tensor, name: str, device=None, dtype=None) -> int:
-    """The row stride of a [rows, cols] operand (0: contiguous)."""
-    _need(t.dim() == 2 and t.is_cuda, f"{name} must be a 2-D CUDA tensor")
-    _need(device is None or t.device == device, f"{name} is on another device")
-    _need(dtype is None or t.dtype == dtype, f"{name} must be {dtype}")
-    _need(t.shape[1] > 0, f"{name} has no columns")
-    _need(t.stride(1) == 1 or t.shape[1] == 1 or t.shape[0] == 0, f"{name} must be contiguous in its last dimension")
-    if t.shape[0] <= 1:
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, row stride) of a matrix; the stride of a single row is 0, contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, not of shape {tuple(shape)}")
+    n, c = shape
+    if c < 1:
+        raise ValueError(f"{name} has no columns")
+    if n <= 1:
+        if n and stride[1] != 1 and c > 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        return n, c, 0
+    if (stride[1] != 1 and c > 1) or stride[0] < c:
+        raise ValueError(f"{name} must be contiguous in its last dimension, with rows that do not overlap")
+    return n, c, stride[0]
+
+
+def _weights(t: torch.Tensor, name: str):
+    """(E, d_out, d_in, row stride, expert stride) of weights [E, d_out, d_in]."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [E, d_out, d_in], not of shape {tuple(shape)}")
+    E, O, I = shape
+    if not 1 <= E <= L.TILEQ_GROUPED_MAX_E or O < 1 or I < 1:
+        raise ValueError(f"{name}: 1 to {L.TILEQ_GROUPED_MAX_E} experts and no empty widths, not {tuple(shape)}")
+    ld = stride[1] if O > 1 else I
+    if (stride[2] != 1 and I > 1) or ld < I or (E > 1 and stride[0] < (O - 1) * ld + I):
+        raise ValueError(f"{name} must be contiguous in its last dimension, with rows that do not overlap")
+    return E, O, I, ld, (stride[0] if E > 1 else 0)
+
+
+def _vector(t, n: int, dtype, name: str, device) -> int:
+    """Pointer of a contiguous vector of n values, 0 for none."""
+    if t is None:
         return 0
-    _need(t.stride(0) >= t.shape[1], f"{name} has overlapping rows")
-    return t.stride(0)
+    if t.dtype is not dtype or t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {device}")
+    return t.data_ptr()
 
 
-def _weights(t: torch.Tensor, name: str, device, dtype=None):
-    """(row stride, expert stride) of [E, d_out, d_in] weights."""
-    _need(t.dim() == 3 and t.is_cuda, f"{name} must be a 3-D CUDA tensor [E, d_out, d_in]")
-    _need(t.device == device, f"{name} is on another device")
-    _need(dtype is None or t.dtype == dtype, f"{name} must be {dtype}")
-    E, O, I = t.shape
-    _need(1 <= E <= L.TILEQ_GROUPED_MAX_E and O > 0 and I > 0, f"{name}: 1 to {L.TILEQ_GROUPED_MAX_E} experts, no empty widths")
-    _need(t.stride(2) == 1 or I == 1, f"{name} must be contiguous in its last dimension")
-    ld = t.stride(1) if O > 1 else I
-    _need(ld >= I and (E == 1 or t.stride(0) >= (O - 1) * ld + I), f"{name} has overlapping rows")
-    return ld, (t.stride(0) if E > 1 else 0)
-
-
-def _offsets(t, E: int, device):
-    _need(t.dim() == 1 and t.shape[0] == E + 1 and t.dtype == torch.int32 and t.device == device and t.is_contiguous(),
-          f"expert_offsets must be a contiguous int32 tensor of {E + 1} values on the operands' device")
-    return t
-
-
-def _code(dtype, default):
-    dtype = default if dtype is None else dtype
-    _need(dtype in _CODE, "out_dtype must be bfloat16, float16 or float32")
-    return dtype
-
-
-class _Call:
-    """The stream of a call, with its device current; new outputs belong to that stream."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-        self.ctx = None
-        if isinstance(stream, int):
-            self.stream = torch.cuda.ExternalStream(stream, device=device)
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
-
-
-def _out(out, shape, dtype, device, name="out"):
+def _result(out, out_dtype, default, shape, like: torch.Tensor) -> torch.Tensor:
+    """The given result, checked, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(tuple(out.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
-    _need(out.dtype == dtype and out.device == device, f"{name} must be {dtype} on {device}")
+        dtype = default if out_dtype is None else out_dtype
+        if dtype not in _CODE:
+            raise ValueError("out_dtype must be bfloat16, float16 or float32")
+        return like.new_empty(shape) if dtype is like.dtype else torch.empty(shape, dtype=dtype, device=like.device)
+    if out.dtype not in _CODE or (out_dtype is not None and out.dtype is not out_dtype):
+        raise ValueError("out must be bfloat16, float16 or float32, as out_dtype says")
+    if out.device != like.device or out.shape != shape:
+        raise ValueError(f"out must be of shape {tuple(shape)} on {like.device}")
     return out
 
 
-def _operand(t, name):
-    _need(t.dtype in (torch.bfloat16, torch.float16), f"{name} must be bfloat16 or float16")
+def _same(a: torch.Tensor, b: torch.Tensor, what: str):
+    if a.dtype is not b.dtype or a.device != b.device:
+        raise ValueError(f"{what} must have the same type and device")
+
+
+def _operand(t: torch.Tensor, name: str) -> int:
+    code = _OPERAND.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16")
+    return code
 
 
 def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """y [P, d_out] with y[p] = W_e x[p]: x [P, d_in], w [E, d_out, d_in]."""
-    _operand(x, "x")
-    ld_x = _rows(x, "x")
+    code = _operand(x, "x")
+    P, I, ld_x = _rows(x, "x")
+    E, O, Iw, ld_w, stride_w = _weights(w, "w")
+    _same(x, w, "x and w")
+    if I != Iw:
+        raise ValueError(f"x has {I} columns, w expects {Iw}")
     dev = x.device
-    ld_w, stride_w = _weights(w, "w", dev, x.dtype)
-    P, I = x.shape
-    E, O, Iw = w.shape
-    _need(I == Iw, f"x has {I} columns, w expects {Iw}")
-    off = _offsets(expert_offsets, E, dev)
-    dt = _code(out_dtype if out_dtype is not None else (out.dtype if out is not None else None), x.dtype)
-    with _Call(dev, stream) as st:
-        y = _out(out, (P, O), dt, dev)
-        g = L.tileq_grouped(_CODE[x.dtype], _CODE[dt], E, P, I, O, ld_x, _rows(y, "out"), ld_w, stride_w, off.data_ptr())
+    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
+
+    def call(st):
+        y = _result(out, out_dtype, x.dtype, (P, O), x)
+        g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
         L.tileq_grouped_gemm(g, x, w, y, _status_word(dev), st)
-    return y
+        return y
+    return _on_stream(dev, stream, call)
 
 
 def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """dx [P, d_in] with dx[p] = W_e^T dy[p]: dy [P, d_out], w [E, d_out, d_in]."""
-    _operand(dy, "dy")
-    ld_y = _rows(dy, "dy")
+    code = _operand(dy, "dy")
+    P, O, ld_y = _rows(dy, "dy")
+    E, Ow, I, ld_w, stride_w = _weights(w, "w")
+    _same(dy, w, "dy and w")
+    if O != Ow:
+        raise ValueError(f"dy has {O} columns, w expects {Ow}")
     dev = dy.device
-    ld_w, stride_w = _weights(w, "w", dev, dy.dtype)
-    P, O = dy.shape
-    E, Ow, I = w.shape
-    _need(O == Ow, f"dy has {O} columns, w expects {Ow}")
-    off = _offsets(expert_offsets, E, dev)
-    dt = _code(out_dtype if out_dtype is not None else (out.dtype if out is not None else None), dy.dtype)
-    with _Call(dev, stream) as st:
-        dx = _out(out, (P, I), dt, dev)
-        g = L.tileq_grouped(_CODE[dy.dtype], _CODE[dt], E, P, I, O, _rows(dx, "out"), ld_y, ld_w, stride_w, off.data_ptr())
+    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
+
+    def call(st):
+        dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
+        g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, _rows(dx, "out")[2], ld_y, ld_w, stride_w, off)
         L.tileq_grouped_gemm_dx(g, dy, w, dx, _status_word(dev), st)
-    return dx
+        return dx
+    return _on_stream(dev, stream, call)
 
 
 def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None):
     """dW [E, d_out, d_in] with dW_e = sum over the rows p of e of dy[p] x[p]^T, zeros for an expert without rows."""
-    _operand(x, "x")
-    ld_x = _rows(x, "x")
-    dev = x.device
-    ld_y = _rows(dy, "dy", dev, x.dtype)
-    _need(x.shape[0] == dy.shape[0], "x and dy must have the same number of rows")
-    (P, I), O = x.shape, dy.shape[1]
-    E = expert_offsets.shape[0] - 1 if expert_offsets.dim() == 1 else 0
-    _need(1 <= E <= L.TILEQ_GROUPED_MAX_E, f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
-    off = _offsets(expert_offsets, E, dev)
-    dt = _code(out_dtype if out_dtype is not None else (out.dtype if out is not None else None), x.dtype)
-    with _Call(dev, stream) as st:
-        dw = _out(out, (E, O, I), dt, dev)
-        ld_w, stride_w = _weights(dw, "out", dev)
-        g = L.tileq_grouped(_CODE[x.dtype], _CODE[dt], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off.data_ptr())
+    code = _operand(x, "x")
+    P, I, ld_x = _rows(x, "x")
+    Py, O, ld_y = _rows(dy, "dy")
+    _same(x, dy, "x and dy")
+    if P != Py:
+        raise ValueError(f"x has {P} rows, dy {Py}")
+    dev, E = x.device, expert_offsets.numel() - 1
+    if not 1 <= E <= L.TILEQ_GROUPED_MAX_E:
+        raise ValueError(f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
+    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
+
+    def call(st):
+        dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
+        ld_w, stride_w = _weights(dw, "out")[3:]
+        g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
         L.tileq_grouped_gemm_dw(g, x, dy, dw, _status_word(dev), st)
-    return dw
+        return dw
+    return _on_stream(dev, stream, call)
 
 
-def _quantised(q, shape, device):
-    """A new e4m3 tensor whose rows start at multiples of 16 bytes, as the product reads them, or the given one."""
+# ------------------------------------------------------------------ fp8
+def _quantised(q, shape, like: torch.Tensor) -> torch.Tensor:
+    """The given e4m3 tensor, checked, or a new one whose rows start at multiples of 16 bytes, as the product reads them."""
     if q is None:
-        q = torch.empty((*shape[:-1], -(-shape[-1] // 16) * 16), dtype=torch.float8_e4m3fn, device=device)
-        return q if q.shape[-1] == shape[-1] else q[..., :shape[-1]]
-    return _out(q, shape, torch.float8_e4m3fn, device)
+        width = shape[-1]
+        if width % 16 == 0:
+            return torch.empty(shape, dtype=_F8, device=like.device)
+        return like.new_empty((*shape[:-1], -(-width // 16) * 16), dtype=_F8)[..., :width]
+    if q.dtype is not _F8 or q.device != like.device or q.shape != shape:
+        raise ValueError(f"out must be float8_e4m3fn of shape {tuple(shape)} on {like.device}")
+    return q
 
 
-def _scales(s, shape, device, name="scales"):
-    if s is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
-    _need(tuple(s.shape) == tuple(shape) and s.dtype == torch.float32 and s.device == device and s.stride(-1) == 1,
-          f"{name} must be a float32 tensor {tuple(shape)} on {device}, contiguous in its last dimension")
-    _need(s.dim() > 2 or s.shape[0] <= 1 or s.stride(0) >= s.shape[1], f"{name} has overlapping rows")
-    return s
-
-
-def _vector(t, n: int, dtype, name: str, device):
-    if t is None:
-        return None
-    _need(t.dim() == 1 and t.shape[0] == n and t.dtype == dtype and t.device == device and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of {n} values on the operands' device")
-    return t.data_ptr()
+def _scales(s, shape, device, name: str) -> int:
+    """Row stride of a given scale tensor (0 where it has one row)."""
+    if s.dtype is not torch.float32 or s.device != device or s.shape != shape:
+        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on {device}")
+    if len(shape) > 2:
+        if not s.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return 0
+    stride = s.stride()
+    if (stride[1] != 1 and shape[1] > 1) or (shape[0] > 1 and stride[0] < shape[1]):
+        raise ValueError(f"{name} must be contiguous in its last dimension, with rows that do not overlap")
+    return stride[0] if shape[0] > 1 else 0
 
 
 def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=None, stream=None):
@@ -231,43 +245,52 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     or fp32.  rows: int32 [R], the row of x of each row of q (outside [0, T): zeros); without it
     R = T.  row_scale: fp32 [R], a factor of each row of q.
     """
-    _need(x.dtype in _CODE, "x must be bfloat16, float16 or float32")
-    ld_x, dev = _rows(x, "x"), x.device
-    T, C = x.shape
+    code = _CODE.get(x.dtype)
+    if code is None:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    T, C, ld_x = _rows(x, "x")
+    dev = x.device
     if swiglu:
-        _need(C % 2 == 0, "x must hold the gate's and the up projection's columns")
+        if C % 2:
+            raise ValueError("x must hold the gate's and the up projection's columns")
         C //= 2
     R = T if rows is None else rows.numel()
     at = _vector(rows, R, torch.int32, "rows", dev)
     factor = _vector(row_scale, R, torch.float32, "row_scale", dev)
-    with _Call(dev, stream) as st:
-        q = _quantised(out, (R, C), dev)
-        s = _scales(scales, (-(-C // 128), R), dev)
-        a = L.tileq_fp8_rows(_CODE[x.dtype], R, T, C, int(bool(swiglu)), at, factor, ld_x, _rows(q, "out"),
-                             s.stride(0) if s.shape[0] > 1 else 0)
+    shape = (-(-C // 128), R)
+
+    def call(st):
+        q = _quantised(out, (R, C), x)
+        s = torch.empty(shape, dtype=torch.float32, device=dev) if scales is None else scales
+        ld_s = _scales(s, shape, dev, "scales")
+        a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out")[2], ld_s)
         L.tileq_fp8_quantize(a, x, q, s, st)
-    return q, s
+        return q, s
+    return _on_stream(dev, stream, call)
 
 
 def fp8_quantize_weights(w, out=None, scales=None, stream=None):
     """Weights [E, d_out, d_in] (or one expert's [d_out, d_in]) in e4m3 with a scale for every 128 x 128 block:
     (q like w, scales [E, ceil(d_out / 128), ceil(d_in / 128)], without E for one)."""
-    _need(w.dtype in _CODE, "w must be bfloat16, float16 or float32")
+    code = _CODE.get(w.dtype)
+    if code is None:
+        raise ValueError("w must be bfloat16, float16 or float32")
     if w.dim() == 2:
         q, s = fp8_quantize_weights(w[None], None if out is None else out[None], None if scales is None else scales[None],
                                     stream)
         return q[0], s[0]
-    dev = w.device
-    ld_w, stride_w = _weights(w, "w", dev)
-    E, O, I = w.shape
-    with _Call(dev, stream) as st:
-        q = _quantised(out, (E, O, I), dev)
-        ld_q, stride_q = _weights(q, "out", dev)
-        s = _scales(scales, (E, -(-O // 128), -(-I // 128)), dev)
-        _need(s.is_contiguous(), "scales must be contiguous")
-        g = L.tileq_grouped(_CODE[w.dtype], 0, E, 0, I, O, 0, 0, ld_w, stride_w, None)
+    E, O, I, ld_w, stride_w = _weights(w, "w")
+    dev, shape = w.device, (E, -(-O // 128), -(-I // 128))
+
+    def call(st):
+        q = _quantised(out, (E, O, I), w)
+        ld_q, stride_q = _weights(q, "out")[3:]
+        s = torch.empty(shape, dtype=torch.float32, device=dev) if scales is None else scales
+        _scales(s, shape, dev, "scales")
+        g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
         L.tileq_fp8_quantize_weights(g, w, q, ld_q, stride_q, s, st)
-    return q, s
+        return q, s
+    return _on_stream(dev, stream, call)
 
 
 def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stream=None):
@@ -276,26 +299,25 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
 
     Dense, without expert_offsets: wq [d_out, d_in], ws [ceil(d_out / 128), ceil(d_in / 128)].
     """
-    if wq.dim() == 2:
-        _need(expert_offsets is None, "a 2-D wq is one expert's, for all rows: no expert_offsets")
+    if (wq.dim() == 2) != (expert_offsets is None):
+        raise ValueError("a product by expert takes wq [E, d_out, d_in] and expert_offsets, a dense one wq [d_out, d_in]")
+    if expert_offsets is None:
         wq, ws = wq[None], ws[None]
-    else:
-        _need(expert_offsets is not None, "expert_offsets say which rows are whose")
-    f8 = torch.float8_e4m3fn
-    _need(xq.dtype == f8, "xq must be float8_e4m3fn")
-    ld_x, dev = _rows(xq, "xq"), xq.device
-    ld_w, stride_w = _weights(wq, "wq", dev, f8)
-    P, I = xq.shape
-    E, O, Iw = wq.shape
-    _need(I == Iw, f"xq has {I} columns, wq expects {Iw}")
-    kb = -(-I // 128)
-    _scales(xs, (kb, P), dev, "xs")
+    if xq.dtype is not _F8:
+        raise ValueError("xq must be float8_e4m3fn")
+    P, I, ld_x = _rows(xq, "xq")
+    E, O, Iw, ld_w, stride_w = _weights(wq, "wq")
+    _same(xq, wq, "xq and wq")
+    if I != Iw:
+        raise ValueError(f"xq has {I} columns, wq expects {Iw}")
+    dev, kb = xq.device, -(-I // 128)
+    ld_xs = _scales(xs, (kb, P), dev, "xs")
     _scales(ws, (E, -(-O // 128), kb), dev, "ws")
-    _need(ws.is_contiguous(), "ws must be contiguous")
-    off = None if expert_offsets is None else _offsets(expert_offsets, E, dev).data_ptr()
-    dt = _code(out_dtype if out_dtype is not None else (out.dtype if out is not None else None), torch.bfloat16)
-    with _Call(dev, stream) as st:
-        y = _out(out, (P, O), dt, dev)
-        g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[dt], E, P, I, O, ld_x, _rows(y, "out"), ld_w, stride_w, off)
-        L.tileq_fp8_gemm(g, xq, xs, xs.stride(0) if kb > 1 else 0, wq, ws, y, _status_word(dev), st)
-    return y
+    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
+
+    def call(st):
+        y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
+        g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
+        L.tileq_fp8_gemm(g, xq, xs, ld_xs, wq, ws, y, _status_word(dev), st)
+        return y
+    return _on_stream(dev, stream, call)
