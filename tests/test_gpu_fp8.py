@@ -106,6 +106,16 @@ def test_gather_padding_and_factors(tq, C):
     assert torch.equal(s.double(), rs) and _same(q, rq)
 
 
+def test_all_padding(tq):
+    """Row numbers into an x without rows: zeros, with scales of 1."""
+    import torch
+    x = torch.empty(0, 384, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(11, dtype=torch.int32, device="cuda")
+    out = torch.full((11, 384), 3.0, device="cuda").to(torch.float8_e4m3fn)
+    q, s = tq.fp8_quantize(x, rows=rows, row_scale=torch.full((11,), float("nan"), device="cuda"), out=out)
+    assert (q.float() == 0).all() and (s == 1).all()
+
+
 def test_rows_strides(tq):
     import torch
     base = _rng(3)(20, 700).to(torch.float16)

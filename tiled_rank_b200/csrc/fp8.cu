@@ -9,8 +9,6 @@
 // bit of its range below 2^-6.  Both kernels are one pass over the data: a block
 // stays in registers between its maximum and its rounding, and what bounds them
 // is memory (2 or 4 bytes in, 1 byte out per value).
-#include <cuda_fp8.h>
-
 #include "fp8.cuh"
 #include "kernels.cuh"
 
@@ -20,31 +18,36 @@ namespace {
 // Eight consecutive values as loaded (two 16-byte words of fp32, one of 16 bits), and widened.
 template <int DT>
 struct Raw8 {
-  uint4 w[DT == TILEQ_DT_F32 ? 2 : 1];
+  static constexpr int W = DT == TILEQ_DT_F32 ? 2 : 1;
+  uint4 w[W];
 };
-// VEC: one or two 16-byte loads where `live`; else value by value, `n` of them.  Zeros behind the end.
-template <int DT, bool VEC>
-__device__ __forceinline__ Raw8<DT> load8(const void *base, long long at, int n) {
+template <int DT>
+__device__ __forceinline__ const char *address(const void *base, long long at) {
+  return reinterpret_cast<const char *>(base) + at * (DT == TILEQ_DT_F32 ? 4 : 2);
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const char *p) {
   Raw8<DT> r;
-  if constexpr (VEC) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + at * (DT == TILEQ_DT_F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < (DT == TILEQ_DT_F32 ? 2 : 1); ++i) r.w[i] = n > 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < Raw8<DT>::W; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+  return r;
+}
+// n of the eight values, one by one; zeros behind them.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_some(const char *p, int n) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0;
+    if (i < n)
+      v[i] = DT == TILEQ_DT_F32 ? reinterpret_cast<const uint32_t *>(p)[i] : reinterpret_cast<const uint16_t *>(p)[i];
+  }
+  Raw8<DT> r;
+  if constexpr (DT == TILEQ_DT_F32) {
+    r.w[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    r.w[1] = make_uint4(v[4], v[5], v[6], v[7]);
   } else {
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0;
-      if (i < n)
-        v[i] = DT == TILEQ_DT_F32 ? reinterpret_cast<const uint32_t *>(base)[at + i]
-                                  : reinterpret_cast<const uint16_t *>(base)[at + i];
-    }
-    if constexpr (DT == TILEQ_DT_F32) {
-      r.w[0] = make_uint4(v[0], v[1], v[2], v[3]);
-      r.w[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    } else {
-      r.w[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-    }
+    r.w[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }
   return r;
 }
@@ -74,62 +77,19 @@ __device__ __forceinline__ void widen(const Raw8<DT> &r, float (&v)[8]) {
   }
 }
 
-// Bits of max |v|: as integers, so that a NaN or an infinity wins.
+// A maximum travels as 16 bits: the upper half of its fp32 pattern with a lowest bit that says whether anything
+// was below it.  That keeps the order and all that the scale depends on (the exponent, and whether the significand
+// is above 1.75), and two blocks' maxima fit one register on their way through the shuffles.
+__device__ __forceinline__ uint32_t top16(uint32_t bits) { return (bits | ((bits & 0xffffu) + 0xffffu)) >> 16; }
+
+// Bits of max |v|, a NaN above all.
 __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
+  for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(m) : "f"(fabsf(v[i])));
+  return __float_as_uint(m) & 0x7fffffffu;
 }
-
-// Scale of a block from the bits of its maximum, and the factor 1 / scale.  With amax = 1.m * 2^k and
-// 448 = 1.75 * 2^8 the scale's exponent is k - 8, one more if 1.m > 1.75.  A block with a NaN or an
-// infinity becomes NaN as a whole.
-__device__ __forceinline__ float scale_of(uint32_t amax, float &inv) {
-  if (amax == 0) return inv = 1.f;
-  if (amax >= 0x7f800000u) return inv = __uint_as_float(0x7fffffffu);
-  const int e = max((int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
-  inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  return __uint_as_float((uint32_t)e << 23);
-}
-
-__device__ __forceinline__ uint2 round8(const float (&v)[8], float inv) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t *q, int n, uint2 w) {
-  if constexpr (VEC) {
-    if (n > 0) *reinterpret_cast<uint2 *>(q) = w;
-  } else {
-    const unsigned long long b = (unsigned long long)w.y << 32 | w.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) q[i] = (uint8_t)(b >> 8 * i);
-  }
-}
-
-constexpr int kQRows = 8;    // rows of a CTA, a warp each
-constexpr int kQCols = 1024; // columns of a CTA: four 16-byte loads a lane, issued before the first is used
-constexpr int kQU = kQCols / 256;
-
-// A warp reads 256 columns at a time, 16 lanes a block of 128.  The scales of
-// eight rows leave together: neighbouring rows are neighbours in a scale row, and
-// single 4-byte stores would each cost a 32-byte sector.
-// VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
-// What a value goes through is what the gathered case pays for: x comes from L2
-// for all but the first of a token's rows, so it is bound by instructions, not by
-// HBM.  16-bit values without a factor therefore stay in pairs: the maxima of two
-// blocks travel through the shuffles in the halves of one register, and bf16 is
-// scaled before it is widened (exact: a power of two; below bf16's normal range
-// the result is zero in e4m3 either way).
-enum QuantKind { Q_PLAIN = 0, Q_FACTOR = 1, Q_SWIGLU = 2 };
-
-// Maxima of the magnitudes of two loads (16-bit bit patterns, NaN on top): low half a's, high half b's.
+// Two loads of 16-bit values: low half the pattern of a's largest magnitude, high half b's.
 template <int DT>
 __device__ __forceinline__ uint32_t amax_pair(const Raw8<DT> &a, const Raw8<DT> &b) {
   const auto top = [](const uint4 &w) {
@@ -140,30 +100,166 @@ __device__ __forceinline__ uint32_t amax_pair(const Raw8<DT> &a, const Raw8<DT> 
   return __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
 }
 
+// Scale of a block from its maximum (top16), and the factor 1 / scale.  With amax = 1.m * 2^k and 448 = 1.75 * 2^8
+// the scale's exponent is k - 8, one more if 1.m > 1.75: 0x1f carries into the exponent just then.
+__device__ __forceinline__ float scale_of(uint32_t top, float &inv) {
+  const int e = max((int)((top + 0x1fu) >> 7) - 8, 1);
+  inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  float s = __uint_as_float((uint32_t)e << 23);
+  if (top - 1u >= 0x7f7fu) {                    // zero, infinity or NaN
+    s = __uint_as_float(top ? 0x7fffffffu : 0x3f800000u);
+    if (top) inv = s;                           // the block becomes NaN as a whole
+  }
+  return s;
+}
+
+// Four fp32 values to e4m3 (nearest even, cut to +-448), in the order of memory.
+__device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ uint2 round8(const float (&v)[8], float inv) {
+  return make_uint2(round4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    round4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+// bf16 is scaled before it is widened (exact: a power of two; below bf16's normal range the result is zero in e4m3
+// either way).
 template <int DT>
-__device__ __forceinline__ uint2 round8_pairs(const Raw8<DT> &r, float inv) {
+__device__ __forceinline__ uint2 round8(const Raw8<DT> &r, float inv) {
+  float v[8];
   if constexpr (DT == TILEQ_DT_BF16) {
     const __nv_bfloat162 f = __float2bfloat162_rn(inv);
     const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-    uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), f);
       const uint32_t u = *reinterpret_cast<const uint32_t *>(&p);
-      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)),
-                                      __NV_SATFINITE, __NV_E4M3);
+      v[2 * i] = __uint_as_float(u << 16);
+      v[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
     }
-    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    return make_uint2(round4(v[0], v[1], v[2], v[3]), round4(v[4], v[5], v[6], v[7]));
   } else {
-    float v[8];
     widen<DT>(r, v);
     return round8(v, inv);
   }
 }
+__device__ __forceinline__ void store_some(uint8_t *q, int n, uint2 w) {
+  const unsigned long long b = (unsigned long long)w.y << 32 | w.x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) q[i] = (uint8_t)(b >> 8 * i);
+}
 
+// g / (1 + exp(-g)) as num / d with e = exp(-|g|), d = 1 + e in [1, 2] and num = g or g e: no value of g leaves the
+// range in which the reciprocal and one correction with the exact remainder give the quotient (the division's own
+// sequence costs twice as much).  An infinite g gives NaN, which its block becomes in any case.
+__device__ __forceinline__ float silu(float g) {
+  const float e = expf(-fabsf(g)), d = 1.f + e, num = g < 0.f ? g * e : g;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(d));
+  const float q = num * r;
+  return fmaf(fmaf(-q, d, num), r, q);
+}
+
+enum QuantKind { Q_PLAIN = 0, Q_FACTOR = 1, Q_SWIGLU = 2 };
+
+constexpr int kQRows = 8;    // rows of a CTA, a warp each
+constexpr int kQCols = 1024; // columns of a CTA: four 16-byte loads a lane, issued before the first is used
+constexpr int kQU = kQCols / 256;
+
+// A warp's 1024 columns of a row, 16 lanes a block of 128.  x, up: this lane's first value of the gate (or the row)
+// and of the up projection; n: values from this lane's first column to the end of the row.
+// FULL: all 1024 are there and aligned.
+template <int DT, QuantKind KIND, bool VEC, bool FULL>
+__device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_t *q, int n, bool live, float factor,
+                                           float *sc, int lane) {
+  constexpr bool SWIGLU = KIND == Q_SWIGLU, PAIRS = KIND == Q_PLAIN && DT != TILEQ_DT_F32;
+  constexpr int ES = DT == TILEQ_DT_F32 ? 4 : 2;
+  Raw8<DT> raw[kQU], ups[SWIGLU ? kQU : 1];
+  auto load = [&](const char *p, int u) {
+    if constexpr (FULL) return load8<DT>(p + u * 256 * ES);
+    // past the end the row's last eight values once more: they are in the block already, or the block is not there
+    if constexpr (VEC) return load8<DT>(p + min(u * 256, n - 8) * ES);
+    return load_some<DT>(p + u * 256 * ES, n - u * 256);
+  };
+  if (live) {
+#pragma unroll
+    for (int u = 0; u < kQU; ++u) {
+      raw[u] = load(x, u);
+      if constexpr (SWIGLU) ups[u] = load(up, u);
+    }
+  } else {  // padding: a row of zeros, whatever its factor
+#pragma unroll
+    for (int u = 0; u < kQU; ++u)
+#pragma unroll
+      for (int i = 0; i < Raw8<DT>::W; ++i) {
+        raw[u].w[i] = make_uint4(0, 0, 0, 0);
+        if constexpr (SWIGLU) ups[u].w[i] = make_uint4(0, 0, 0, 0);
+      }
+    if constexpr (KIND != Q_PLAIN) factor = 1.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kQU; u += 2) {
+    float v[2][8];
+    uint32_t m;
+    if constexpr (PAIRS) {
+      m = amax_pair<DT>(raw[u], raw[u + 1]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        widen<DT>(raw[u + h], v[h]);
+        if constexpr (SWIGLU) {
+          float b[8];
+          widen<DT>(ups[u + h], b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[h][i] = silu(v[h][i]) * b[i];
+        }
+        if constexpr (KIND != Q_PLAIN) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[h][i] *= factor;
+        }
+      }
+      m = top16(amax8(v[0])) | top16(amax8(v[1])) << 16;
+    }
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t top = h ? m >> 16 : m & 0xffffu;
+      if constexpr (PAIRS && DT == TILEQ_DT_F16) top = top16(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))));
+      float inv;
+      const float s = scale_of(top, inv);
+      uint2 w;
+      if constexpr (PAIRS)
+        w = round8<DT>(raw[u + h], inv);
+      else
+        w = round8(v[h], inv);
+      uint8_t *to = q + (u + h) * 256;
+      if constexpr (FULL) {
+        *reinterpret_cast<uint2 *>(to) = w;
+      } else if constexpr (VEC) {
+        if (n > (u + h) * 256) *reinterpret_cast<uint2 *>(to) = w;
+      } else {
+        store_some(to, n - (u + h) * 256, w);
+      }
+      if ((lane & 15) == 0) sc[((u + h) * 2 + (lane >> 4)) * kQRows] = s;
+    }
+  }
+}
+
+// One CTA per eight rows x 1024 columns, columns in the outer order: a slice of x that many rows are gathered from
+// stays in L2.  Gathered rows are then bound by instructions rather than by HBM, hence the 16-bit maxima and the
+// path for whole parts without any check.  (Persistent CTAs with the next item's loads in flight were slower, 276
+// against 195 us at 131072 x 4096: their registers leave a third of the warps.)
+// The scales of eight rows leave together: neighbouring rows are neighbours in a scale row, and single 4-byte
+// stores would each cost a 32-byte sector.
+// VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
 template <int DT, QuantKind KIND, bool VEC>
 __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRowsArgs P) {
-  constexpr bool SWIGLU = KIND == Q_SWIGLU, PAIRS = KIND == Q_PLAIN && DT != TILEQ_DT_F32;
   __shared__ float sc[kQCols / 128][kQRows];
   pdl_wait_and_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,55 +267,19 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
   const int c0 = blockIdx.y * kQCols;
   if (r < P.R) {
     const long long src = P.rows ? P.rows[r] : r;
-    const bool live = src >= 0 && src < P.T;  // a row number outside x is padding: a row of zeros
-    Raw8<DT> raw[kQU], up[SWIGLU ? kQU : 1];
-#pragma unroll
-    for (int u = 0; u < kQU; ++u) {
-      const int c = c0 + u * 256 + lane * 8;
-      raw[u] = load8<DT, VEC>(P.x, src * P.ld_x + c, live ? P.C - c : 0);
-      if constexpr (SWIGLU) up[u] = load8<DT, VEC>(P.x, src * P.ld_x + P.C + c, live ? P.C - c : 0);
-    }
-    uint8_t *q = P.q + r * P.ld_q + c0 + lane * 8;
+    const bool live = src >= 0 && src < P.T;  // a row number outside x is padding
     const int n = P.C - c0 - lane * 8;
-    if constexpr (PAIRS) {
-#pragma unroll
-      for (int u = 0; u < kQU; u += 2) {
-        uint32_t m = amax_pair<DT>(raw[u], raw[u + 1]);
-#pragma unroll
-        for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t top = h ? m >> 16 : m & 0xffffu;
-          float inv;
-          const float s = scale_of(DT == TILEQ_DT_BF16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half((uint16_t)top))), inv);
-          store8<VEC>(q + (u + h) * 256, n - (u + h) * 256, round8_pairs<DT>(raw[u + h], inv));
-          if ((lane & 15) == 0) sc[(u + h) * 2 + (lane >> 4)][warp] = s;
-        }
-      }
+    const char *x = address<DT>(P.x, (live ? src : 0) * P.ld_x + c0 + lane * 8);
+    const char *up = address<DT>(x, P.C);
+    uint8_t *q = P.q + r * P.ld_q + c0 + lane * 8;
+    const float factor = KIND != Q_PLAIN && P.row_scale ? P.row_scale[r] : 1.f;
+    if constexpr (VEC) {
+      if (c0 + kQCols <= P.C)
+        quant_part<DT, KIND, true, true>(x, up, q, n, live, factor, &sc[0][warp], lane);
+      else
+        quant_part<DT, KIND, true, false>(x, up, q, n, live, factor, &sc[0][warp], lane);
     } else {
-      const float w = P.row_scale ? P.row_scale[r] : 1.f;
-#pragma unroll
-      for (int u = 0; u < kQU; ++u) {
-        float v[8];
-        widen<DT>(raw[u], v);
-        if constexpr (SWIGLU) {
-          float b[8];
-          widen<DT>(up[u], b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * b[i];
-        }
-        if (KIND != Q_PLAIN && live) {  // rows of zeros stay zeros, whatever their factor
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= w;
-        }
-        uint32_t m = amax8(v);
-#pragma unroll
-        for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float inv;
-        const float s = scale_of(m, inv);
-        store8<VEC>(q + u * 256, n - u * 256, round8(v, inv));
-        if ((lane & 15) == 0) sc[u * 2 + (lane >> 4)][warp] = s;
-      }
+      quant_part<DT, KIND, false, false>(x, up, q, n, live, factor, &sc[0][warp], lane);
     }
   }
   __syncthreads();
@@ -237,11 +297,19 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
   const long long per = (long long)P.nO * P.nI;
   const int e = (int)(blockIdx.x / per), b = (int)(blockIdx.x % per);
   const int o0 = b / P.nI * 128 + (int)(threadIdx.x >> 4), c = b % P.nI * 128 + (int)(threadIdx.x & 15) * 8;
+  const int n = P.d_in - c;  // values from this thread's first column to the end of the row
   Raw8<DT> raw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int o = o0 + 16 * i;
-    raw[i] = load8<DT, VEC>(P.w, e * P.stride_w + o * P.ld_w + c, o < P.d_out ? P.d_in - c : 0);
+    const char *p = address<DT>(P.w, e * P.stride_w + o * P.ld_w + c);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < Raw8<DT>::W; ++j) raw[i].w[j] = make_uint4(0, 0, 0, 0);
+      if (o < P.d_out && n > 0) raw[i] = load8<DT>(p);
+    } else {
+      raw[i] = load_some<DT>(p, o < P.d_out ? n : 0);
+    }
   }
   float v[8][8];
   uint32_t m = 0;
@@ -257,11 +325,18 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, top[i]);
   float inv;
-  const float s = scale_of(m, inv);
+  const float s = scale_of(top16(m), inv);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int o = o0 + 16 * i;
-    if (o < P.d_out) store8<VEC>(P.q + e * P.stride_q + o * P.ld_q + c, P.d_in - c, round8(v[i], inv));
+    uint8_t *to = P.q + e * P.stride_q + o * P.ld_q + c;
+    if (o < P.d_out) {
+      if constexpr (VEC) {
+        if (n > 0) *reinterpret_cast<uint2 *>(to) = round8(v[i], inv);
+      } else {
+        store_some(to, n, round8(v[i], inv));
+      }
+    }
   }
   if (threadIdx.x == 0) P.scales[blockIdx.x] = s;
 }
