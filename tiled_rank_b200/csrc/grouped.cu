@@ -91,6 +91,11 @@ struct Ring {
   __device__ void next() {
     if (++at == N) at = 0, parity ^= 1;
   }
+  __device__ Ring after() const {
+    Ring r = *this;
+    r.next();
+    return r;
+  }
 };
 
 struct Tile {
@@ -131,11 +136,16 @@ struct Tiles {
   }
 };
 
-// Two barriers asked at once (a single question takes about 100 cycles, also when the answer is yes), then waited for.
-__device__ __forceinline__ bool warp_wait2(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, int *status) {
-  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
-  if (__all_sync(0xffffffffu, ra && rb)) return true;
-  return __all_sync(0xffffffffu, mbar_wait(a, pa, status) && mbar_wait(b, pb, status));
+// Has this phase of the barrier completed?  Asked without waiting; the answer takes some 100 cycles, so the loops ask
+// for what they need next before the work at hand.
+__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // TMEM to registers in the layout of 8 x 8 blocks (16x256b): of 32 lanes x 32
@@ -463,6 +473,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       const int part = PARTS == 2 ? warp - 1 : 0;
       Ring<SQ> q;
       Ring<NACC> acc;
+      bool full_ready = false, acc_ready = false;
       const uint64_t ad0 = tc::sdesc(smem_addr(stage_a(0)), A_MN ? 8192 : 16);
       const uint64_t bd0 = tc::sdesc(smem_addr(stage_b(0)) + part * (G::PC / CG * 128), B_MN ? 8192 : 16);
       for (int w = unit0; ok && tiles.get(w, t); w += units) {
@@ -477,13 +488,19 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
           const uint64_t at = (uint64_t)(q.at * (G::STAGE >> 4));
-          if (mine && first_k && !cut)
-            ok = warp_wait2(&full[q.at], q.parity, &acc_empty[pa], acc.parity ^ 1, P.status);
-          else
+          const bool want_acc = mine && first_k;
+          if (cut || !__all_sync(0xffffffffu, full_ready && (acc_ready || !want_acc)))
             ok = warp_wait(&full[q.at], q.parity, P.status, cut) &&
-                 (!(mine && first_k) || warp_wait(&acc_empty[pa], acc.parity ^ 1, P.status));
+                 (!want_acc || warp_wait(&acc_empty[pa], acc.parity ^ 1, P.status));
           if (!ok) break;
           tc::fence_after();
+          // the next stage's barriers, asked now: the answers come while this one's MMAs are issued
+          const Ring<SQ> q1 = q.after();
+          full_ready = test_wait(&full[q1.at], q1.parity);
+          if (G::F8) {
+            const Ring<NACC> a1 = acc.after();
+            acc_ready = test_wait(&acc_empty[part * NACC + a1.at], a1.parity ^ 1);
+          }
           if (tc::elect_one()) {
             if (mine) {
 #pragma unroll
@@ -594,7 +611,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
               } else {
                 release();
                 // the next block's barrier is asked before the last FMAs, which take as long as the answer
-                ready = mbar_try_wait(&my_full[acc.at], acc.parity);
+                ready = test_wait(&my_full[acc.at], acc.parity);
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) fma2(v[8 * c + i], pair(r[c & 1][2 * i], r[c & 1][2 * i + 1]), ss);
