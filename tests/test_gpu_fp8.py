@@ -208,6 +208,15 @@ def test_products(tq, counts, I, O):
     _check(tq, *_operands(counts, I, O), f"{counts} {I} {O}")
 
 
+@pytest.mark.parametrize("counts,I,O", [([1], 4096, 512), ([7], 2048, 136), ([40], 1104, 264), ([3, 0, 64, 1], 1536, 264),
+                                        ([16, 33], 1008, 1000), ([64], 272, 64)])
+def test_few_tiles_share_a_reduction(tq, counts, I, O):
+    import torch
+    ops = _operands(counts, I, O, seed=I)
+    y = _check(tq, *ops, f"{counts} {I} {O}")
+    assert torch.equal(y, tq.fp8_gemm(*ops))
+
+
 @pytest.mark.parametrize("out_dtype", ["bfloat16", "float16", "float32"])
 def test_product_types_strides_and_other_rows(tq, out_dtype):
     import torch

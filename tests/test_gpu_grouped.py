@@ -52,6 +52,27 @@ def test_products(tq, counts, d_in, d_out, dtype):
     _check_all(tq, x, dy, w, off, f"{counts} {d_in} {d_out}")
 
 
+@pytest.mark.parametrize("counts,d_in,d_out", [([1], 4096, 512), ([7], 2048, 136), ([40], 1096, 264), ([3, 0, 64, 1], 1536, 264),
+                                               ([16, 33], 712, 1000), ([5], 320, 128), ([64], 136, 64)])
+def test_few_tiles_share_a_reduction(tq, counts, d_in, d_out):
+    """Calls with so few tiles that CTAs share the sums of one: long reductions, odd parts, some of them empty."""
+    import torch
+    for dtype in (torch.bfloat16, torch.float16):
+        x, dy, w, off = _make(counts, d_in, d_out, dtype, seed=d_in)
+        _check_all(tq, x, dy, w, off, f"{counts} {d_in} {d_out}")
+
+
+@pytest.mark.parametrize("counts", [[4096], [1000, 0, 3, 500], [129, 2000]])
+def test_weight_gradient_over_many_rows(tq, counts):
+    """dW of small matrices over long sums, which CTAs share."""
+    import torch
+    x, dy, w, off = _make(counts, 136, 72, torch.bfloat16, seed=11)
+    dw = tq.grouped_gemm_dw(x, dy, off)
+    ref, mag = ref_dw(x, dy, off)
+    assert_within(dw, ref, mag, max(counts), "dw")
+    assert torch.equal(dw, tq.grouped_gemm_dw(x, dy, off))
+
+
 @pytest.mark.parametrize("E", [1, 60, 64, 256])
 def test_expert_counts(tq, E):
     import torch

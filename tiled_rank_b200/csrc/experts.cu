@@ -98,20 +98,49 @@ tileq_status check(const tileq_grouped *g, const void *a, const void *b, const v
   return TILEQ_OK;
 }
 
-// The wide kernel (pairs of CTAs, 256 x 256 tiles) needs experts with enough
-// rows to fill its columns; the narrow one (one CTA, 128 x 64) streams the
-// weights of experts with few rows.
-GroupedKernel pick(GroupedMode mode, const tileq_grouped *g, bool fp8) {
-  if (mode == GG_DW) return GG_WIDE;
-  const long long live = std::min(g->E, std::max(g->P, 1));
-  return g->P > (fp8 ? 96 : 48) * live ? GG_WIDE : GG_NARROW;
+// Rows of the experts that have any, at least: the routing is on the device, so the host goes by P and E.
+long long rows_per_expert(const tileq_grouped *g) { return g->P / std::min(g->E, std::max(g->P, 1)); }
+
+// Most tiles of a kernel that the call can have.
+long long tile_count(const GroupedTile &t, GroupedMode mode, const tileq_grouped *g, int contig) {
+  const long long row_tiles = g->P / (t.rows_on_lanes ? t.lanes : t.cols) + std::min(g->E, g->P);
+  const long long other = mode == GG_DW ? g->E * div_up(g->d_out, t.cols) : row_tiles;
+  return div_up(contig, t.rows_on_lanes ? t.cols : t.lanes) * other;
+}
+
+// The wide kernel (256 x 256 tiles of a pair of CTAs; fp8: 128 x 256 of one) needs experts with rows to fill its
+// columns and tiles to fill the GPU; else the narrow one (128 x 64 tiles).  Measured, us narrow / wide:
+//   fwd 8 x 4096 -> 14336:   8 rows an expert 157 / 159, 64 rows 186 / 167;   60 x 2048 -> 1408, 68 rows: 79 / 63
+//   dx  8 x 14336 -> 4096:   16 rows 145 / 139;   60 x 1408 -> 2048, 17 rows: 47.6 / 45.0
+//   fwd 1 x 2048 -> 2048:    256 rows (8 wide tiles) 12.9 / 15.9, 1024 rows (32) 22.7 / 16.7
+//   fp8 8 x 4096 -> 14336:   16 rows 91 / 97, 24 rows 101 / 97, 64 rows 161 / 102
+//   fp8 1 x 2048 -> 2048:    256 rows (16 wide tiles) 12.3 / 14.3, 1024 rows (64) 22.2 / 14.8
+//   dW  512 x 512, 256 rows: 1 expert (4 wide tiles) 6.4 / 8.6, 60 experts (240) 31 / 21
+GroupedKernel pick(GroupedMode mode, const tileq_grouped *g, int contig, bool fp8) {
+  const bool rows = mode == GG_DW || rows_per_expert(g) > (fp8 ? 12 : mode == GG_DX ? 6 : 16);
+  return rows && tile_count(grouped_tile(GG_WIDE, fp8), mode, g, contig) >= (fp8 ? 48 : 24) ? GG_WIDE : GG_NARROW;
+}
+
+// Where the narrow kernel has too few tiles for the GPU, clusters of CTAs share a tile's reduction, if it is long
+// enough: a step takes a CTA about 0.28 us, the sums' meeting 2 us and 0.02 more for every column.  No more clusters
+// than run at the same time (clusters of eight leave SMs idle: 16 of them took two rounds).  Measured, us without /
+// with:  fwd 1 x 4096 -> 1536, 4 rows: 18.9 / 7.9;  1 x 2048 -> 2048, 64 rows: 12.5 / 10.0;  1 x 512 -> 512, 64 rows
+// (8 steps, not taken): 6.9 / 8.2;  dW 512 x 512, 4096 rows: 24.4 / 13.8.
+int pick_splits(GroupedMode mode, const tileq_grouped *g, long long tiles, int reduction, bool fp8) {
+  const long long rows = rows_per_expert(g), steps = div_up(mode == GG_DW ? rows : reduction, fp8 ? 128 : 64);
+  const long long columns = mode == GG_DW ? 64 : std::min(rows, 64ll);
+  int best = 1;
+  for (int s = 2; s <= 8; s *= 2)
+    if (steps >= 2 * s && tiles <= grouped_clusters(mode, fp8, s) && 28 * (steps / best - steps / s) > (best == 1 ? 200 + 2 * columns : 0))
+      best = s;
+  return best;
 }
 
 // contig: the contiguous output dimension; weights and rows: the operands.  The rows' operand lies on the TMEM
 // columns, but for the wide fp8 kernel; GG_DW has no weights among its operands, `weights` is x.
 tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const Operand &weights, const Operand &rows,
                  int contig, bool fp8, cudaStream_t stream) {
-  const GroupedKernel k = pick(mode, g, fp8);
+  const GroupedKernel k = pick(mode, g, contig, fp8);
   const GroupedTile t = grouped_tile(k, fp8);
   const bool on_lanes = t.rows_on_lanes;
   const int cg = t.lanes / 128;
@@ -126,15 +155,16 @@ tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const
   // out is 16-byte aligned; the 32-byte stores of 16 bf16 or 8 fp32 want more
   const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   a.store_words = wide && all(16) ? 16 : all(8) && (wide || g->out_dtype != TILEQ_DT_F32) ? 8 : all(2) ? 2 : 1;
-  const long long row_tiles = g->P / (on_lanes ? t.lanes : t.cols) + std::min(g->E, g->P);  // at most
-  const long long tiles = div_up(contig, on_lanes ? t.cols : t.lanes) * (mode == GG_DW ? g->E * div_up(a.C, t.cols) : row_tiles);
+  const long long tiles = tile_count(t, mode, g, contig);
   if (tiles > (1ll << 30)) return TILEQ_ERR_UNSUPPORTED;
   if (!encode(&a.amap, on_lanes ? rows : weights, mode == GG_FWD ? 128 : 64) ||
       !encode(&a.bmap, on_lanes ? weights : rows, mode == GG_DW ? 64 : t.box_b))
     return TILEQ_ERR_CUDA;
   const int sms = sm_count();
-  if (sms < cg) return TILEQ_ERR_CUDA;
-  const int grid = (int)std::min<long long>(sms / cg, tiles) * cg;
+  if (sms < 8) return TILEQ_ERR_CUDA;
+  a.splits = k == GG_NARROW ? pick_splits(mode, g, tiles, a.R, fp8) : 1;
+  const int group = cg * a.splits;
+  const int grid = (int)std::min<long long>(sms / group, tiles) * group;
   return launch_grouped(a, k, mode, fp8, grid, stream) == cudaSuccess ? TILEQ_OK : TILEQ_ERR_CUDA;
 }
 

@@ -35,6 +35,8 @@
 // are too many columns for that (the reads alone cost more than the MMAs), so
 // there the operands change places: rows of x on the lanes (ROWS), each thread
 // with the scale of its own row in a register.
+// Few tiles, as of one expert's few rows: clusters of CTAs share the reduction of
+// each (SPLIT).
 // Every wait is bounded and reports TILEQ_ERR_TIMEOUT.
 #include "grouped.cuh"
 
@@ -51,10 +53,13 @@ constexpr int kFirstEpw = 4;        // first epilogue warp
 constexpr int kRegsControl = 56, kRegsEpilogue = 224;  // registers a thread where the warps split them
 constexpr int kRowTileGroup = 8;    // column tiles that share a pass over the lane tiles
 
-template <int CG_, int BN_, bool F8_>
+template <int CG_, int BN_, bool F8_, bool SPLIT_ = false>
 struct GCfg {
   static constexpr int CG = CG_, BN = BN_;
   static constexpr bool F8 = F8_;
+  // A cluster of CTAs shares a tile, each with a part of the reduction; their partial sums meet in shared memory.
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int RED = SPLIT ? 128 * BN * 4 : 0;
   static constexpr bool ROWS = F8 && BN == 256;  // the experts' rows on the lanes, d_out on the columns
   static constexpr int LANES = 128 * CG;
   static constexpr int KE = F8 ? 128 : 64;  // reduction elements per stage (128 bytes)
@@ -67,7 +72,7 @@ struct GCfg {
   static constexpr int B_BYTES = BN / CG * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TAB = (2 * kGroupedMaxE + 2) * 4;
-  static constexpr int SQ = (227 * 1024 - TAB - SCALES - 512) / STAGE;
+  static constexpr int SQ = (227 * 1024 - TAB - SCALES - RED - 512) / STAGE;
   // ROWS: the columns of a tile are two MMAs, one for each 128 of d_out and so for each weight scale, with
   // accumulators of their own, folded by four epilogue warps each: while one part is folded the other's MMAs run
   static constexpr int PARTS = ROWS ? 2 : 1;
@@ -76,9 +81,11 @@ struct GCfg {
   static constexpr int NACC = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = NACC * BN;
   static constexpr int BAR_OFF = SQ * STAGE;
-  static constexpr int SCALE_OFF = BAR_OFF + ((3 * SQ + 2 * NACC * PARTS + 1) * 8 + 31) / 16 * 16;
-  static constexpr int TAB_OFF = SCALE_OFF + SCALES;
+  static constexpr int SCALE_OFF = BAR_OFF + ((3 * SQ + 2 * NACC * PARTS + 3) * 8 + 31) / 16 * 16;
+  static constexpr int RED_OFF = SCALE_OFF + SCALES;
+  static constexpr int TAB_OFF = RED_OFF + RED;
   static constexpr int SMEM = TAB_OFF + TAB;
+  static_assert(!SPLIT || (CG == 1 && PARTS == 1 && EPW == 4), "the reduction's columns");
   static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two of tensor memory columns");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -150,11 +157,10 @@ __device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
 
 // TMEM to registers in the layout of 8 x 8 blocks (16x256b): of 32 lanes x 32
 // columns at taddr, r[h][4 j + 2 g + i] is lane 16 h + 8 g + id / 4, column
-// 8 j + 2 (id % 4) + i for thread id.  A thread so holds two neighbouring columns
-// of four lanes: a column's scale is read from shared memory once for four of
-// them, and the block transposes with one instruction for the stores.  (These
-// loads run at half the rate of 32x32b: 550 against 260 cycles for 128 columns
-// in eight warps.)  The values are there after wait_block of the same r.
+// 8 j + 2 (id % 4) + i for thread id: what a transposing store wants.  (These
+// loads run at half the rate of 32x32b, a lane for each thread: 550 against 260
+// cycles for 128 columns in eight warps.  The folds use those.)  The values are
+// there after wait_block of the same r.
 __device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -164,14 +170,7 @@ __device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void ld_half(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void ld_block(uint32_t taddr, uint32_t (&r)[2][N]) {
+__device__ __forceinline__ void ld_block(uint32_t taddr, uint32_t (&r)[2][16]) {
   ld_half(taddr, r[0]);
   ld_half(taddr + (16u << 16), r[1]);
 }
@@ -183,8 +182,7 @@ __device__ __forceinline__ void tie(uint32_t (&r)[16]) {
   tie(*reinterpret_cast<uint32_t(*)[8]>(&r[0]));
   tie(*reinterpret_cast<uint32_t(*)[8]>(&r[8]));
 }
-template <int N>
-__device__ __forceinline__ void wait_block(uint32_t (&r)[2][N]) {
+__device__ __forceinline__ void wait_block(uint32_t (&r)[2][16]) {
   tc::wait_ld();
   tie(r[0]);
   tie(r[1]);
@@ -279,6 +277,52 @@ __device__ __forceinline__ void store_block(const GroupedArgs &P, long long base
   }
 }
 
+// Stores n of N columns where a thread has the values of its own lane (pairs of neighbouring columns): column j to
+// out + at + j * ldo, which is this lane's (in: it exists).  16-bit results of neighbouring lanes are exchanged so that
+// a store takes two of them (PAIR).
+template <int N, int DT, bool PAIR>
+__device__ __forceinline__ void store_lanes_b16(uint16_t *out, long long ldo, int n, bool in, int odd, const uint64_t (&v)[N / 2]) {
+  if constexpr (PAIR) out += odd ? ldo - 1 : 0;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i, out += 2 * ldo) {
+    if (2 * i >= n) break;
+    const float a = low(v[i]), b = high(v[i]);
+    if constexpr (PAIR) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+      const uint32_t w = pack2<DT>(odd ? got : a, odd ? b : got);
+      if (in && 2 * i + odd < n) *reinterpret_cast<uint32_t *>(out) = w;
+    } else {
+      if (in) out[0] = (uint16_t)pack2<DT>(a, 0.f);
+      if (in && 2 * i + 1 < n) out[ldo] = (uint16_t)pack2<DT>(b, 0.f);
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_lanes(const GroupedArgs &P, long long at, int n, bool in, int odd, const uint64_t (&v)[N / 2]) {
+  if (P.out_dtype == TILEQ_DT_F32) {
+    float *out = reinterpret_cast<float *>(P.out) + at;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i, out += 2 * P.ldo) {
+      if (2 * i >= n) break;
+      if (in) out[0] = low(v[i]);
+      if (in && 2 * i + 1 < n) out[P.ldo] = high(v[i]);
+    }
+    return;
+  }
+  uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + at;
+  if (P.out_dtype == TILEQ_DT_BF16) {
+    if (P.store_words >= 2)
+      store_lanes_b16<N, TILEQ_DT_BF16, true>(out, P.ldo, n, in, odd, v);
+    else
+      store_lanes_b16<N, TILEQ_DT_BF16, false>(out, P.ldo, n, in, odd, v);
+  } else {
+    if (P.store_words >= 2)
+      store_lanes_b16<N, TILEQ_DT_F16, true>(out, P.ldo, n, in, odd, v);
+    else
+      store_lanes_b16<N, TILEQ_DT_F16, false>(out, P.ldo, n, in, odd, v);
+  }
+}
+
 // Stores n columns of one output row, N / 2 pairs in registers, to out + base.  A thread has a row of its own, so a
 // store should fill whole 32-byte sectors where the row allows it (WORDS == 16).
 __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
@@ -346,13 +390,16 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   uint64_t *acc_empty = acc_full + PARTS * NACC;  // both [PARTS][NACC]
   uint64_t *tail = acc_empty + PARTS * NACC;  // [SQ] GG_DW: the copies of a stage with foreign rows
   uint64_t *drain = tail + SQ;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *red_full = drain + 1, *red_empty = red_full + 1;  // SPLIT: the partial sums are here, have been read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_empty + 1);
   float *scale = reinterpret_cast<float *>(smem + G::SCALE_OFF);
   int *first = reinterpret_cast<int *>(smem + G::TAB_OFF), *beg = first + kGroupedMaxE + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : tc::cluster_rank();
-  const int unit0 = blockIdx.x / CG, units = gridDim.x / CG;
+  const int splits = G::SPLIT ? P.splits : 1, split = G::SPLIT ? (int)tc::cluster_rank() : 0;
+  const uint32_t lead = CG == 2 ? 0 : split;  // the CTA of the cluster that issues this one's MMAs
+  const int unit0 = blockIdx.x / (CG * splits), units = gridDim.x / (CG * splits);
   auto stage_a = [&](int s) { return smem + s * G::STAGE; };
   auto stage_b = [&](int s) { return smem + s * G::STAGE + G::A_BYTES; };
 
@@ -368,6 +415,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       mbar_init(&acc_empty[b], G::EPW / PARTS * CG);
     }
     mbar_init(drain, PARTS);
+    mbar_init(red_full, G::EPW * splits);
+    mbar_init(red_empty, G::EPW * splits);
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc_cg<CG>(tmem_slot, G::TMEM_COLS);
@@ -400,11 +449,14 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   }
   tc::fence_before();
   __syncthreads();
-  if constexpr (CG == 2) tc::cluster_sync();
+  if constexpr (CG == 2 || G::SPLIT) tc::cluster_sync();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
   auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
+  // this CTA's steps of the reduction
+  auto first_step = [&](int nk) { return G::SPLIT ? nk * split / splits : 0; };
+  auto end_step = [&](int nk) { return G::SPLIT ? nk * (split + 1) / splits : nk; };
   // parts of the tile that have columns, and the columns of one part's MMA
   auto parts = [&](const Tile &t) { return PARTS == 1 || t.ncols <= G::PC ? 1 : 2; };
   auto mma_n = [&](const Tile &t) { return G::ROWS ? G::PC : tiles_of(t.ncols, 16 * CG) * 16 * CG; };
@@ -441,7 +493,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         y = MODE == GG_DW ? t.row0 : 0;
       }
       if (MODE != GG_DW && is_a != G::ROWS) z = t.e;
-      for (int kb = 0; kb < nk; ++kb, q.next()) {
+      const int k0 = first_step(nk), k1 = end_step(nk);
+      x += along_x ? k0 * G::KE : 0;
+      y += along_x ? 0 : k0 * G::KE;
+      for (int kb = k0; kb < k1; ++kb, q.next()) {
         const int left = MODE == GG_DW ? t.rows - kb * G::KE : G::KE;
         const bool cut = left < G::KE && (left & 15);  // the last MMA of the step reaches the next expert's rows
         if (!(ok = warp_wait(&empty[q.at], q.parity ^ 1, P.status))) break;
@@ -481,9 +536,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         const bool mine = part < parts(t);
         const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                                ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
-        for (int kb = 0; kb < nk; ++kb, q.next()) {
+        const int k0 = first_step(nk), k1 = end_step(nk);
+        for (int kb = k0; kb < k1; ++kb, q.next()) {
           const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
-          const bool last = G::F8 || kb == nk - 1, first_k = G::F8 || kb == 0;
+          const bool last = G::F8 || kb == k1 - 1, first_k = G::F8 || kb == k0;
           const int pa = part * NACC + acc.at;
           // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
           const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
@@ -528,8 +584,9 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       uint32_t q0 = 0, phase = 0;  // phase: bit s, the use of tail[s]
       for (int w = unit0; ok && tiles.get(w, t); w += units) {
         const int nk = steps(t), left = t.rows & 63;
-        q0 += nk;
-        if (!(left & 15)) continue;
+        const int k0 = first_step(nk), k1 = end_step(nk);
+        q0 += k1 - k0;
+        if (!(left & 15) || k1 < nk || k0 == k1) continue;  // the last step has all its rows, or is another CTA's
         const int s = (q0 - 1) % SQ, to = (left + 15) & ~15, nbox = (mma_n(t) / CG + 63) / 64;
         if (!(ok = warp_wait(&tail[s], phase >> s & 1, P.status))) break;
         phase ^= 1u << s;
@@ -540,7 +597,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::arrive_at(tc::map_cta(&full[s], 0));
+        if (lane == 0) tc::arrive_at(tc::map_cta(&full[s], lead));
       }
     }
   } else if (warp >= kFirstEpw) {
@@ -553,9 +610,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     const int part = PARTS == 2 ? half : 0;
     uint64_t *my_full = acc_full + part * NACC, *my_empty = acc_empty + part * NACC;
     Ring<NACC> acc;
-    uint32_t group = 0;
+    uint32_t group = 0, red_parity = 0;
     bool ready = false;
-    const uint32_t release_at = tc::map_cta(my_empty, 0);
+    float *red = reinterpret_cast<float *>(smem + G::RED_OFF);
+    const uint32_t release_at = tc::map_cta(my_empty, lead);
     auto release = [&] {  // this warp has read the accumulator (wait::ld is the whole warp's)
       tc::fence_before();
       if (lane == 0) tc::arrive_relaxed_at(release_at + acc.at * 8);
@@ -563,7 +621,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     };
     // (narrow fp8: the four warps of a named barrier stay together, also after a wait that gave up)
     for (int w = unit0; (ok || G::F8) && tiles.get(w, t); w += units) {
-      const int nk = steps(t), l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
+      const int steps_all = steps(t), k0 = first_step(steps_all), nk = end_step(steps_all) - k0;  // this CTA's steps
+      const int l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
       const int cw = half * G::COLS;                  // first column of this warp
       const int mine = min(t.ncols - cw, G::COLS);    // its columns, none if <= 0
       if constexpr (G::ROWS) {
@@ -625,45 +684,100 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         const int nl = P.L - l0;
         const long long base = (MODE == GG_DW ? (long long)t.e * P.out_stride + (long long)(t.c0 + cw) * P.ldo
                                               : (long long)(t.row0 + t.c0 + cw) * P.ldo) + l0;
+        // SPLIT: CTA i of the cluster sums columns [i, i + 1) << shift of the tile.  Each CTA sends its partial sums
+        // there, [sender][four columns][128 lanes][4] so that a lane's four travel as 16 bytes (word by word the
+        // sending took longer than the products); the receiver adds them in the senders' order, so the bits do not
+        // depend on who comes first.
+        int shift = 2;
+        if constexpr (G::SPLIT) {
+          while (splits << shift < t.ncols) ++shift;
+          ok = ok && warp_wait(red_empty, red_parity ^ 1, P.status, true);
+        }
+        [[maybe_unused]] const int tid = threadIdx.x & 127;
+        [[maybe_unused]] auto send = [&](int c, float a, float b, float d, float e) {  // columns c .. c + 3 of this lane
+          if (c < mine)
+            tc::store4_at(tc::map_cta(red, c >> shift) + ((((split << shift) + (c & ((1 << shift) - 1))) >> 2) * 128 + tid) * 16, a, b, d, e);
+        };
+        [[maybe_unused]] auto join = [&](long long base, int nl) {
+          tc::fence_cluster();
+          __syncwarp();
+          if (lane < splits) tc::arrive_at(tc::map_cta(red_full, lane));
+          const bool got = ok && warp_wait(red_full, red_parity, P.status, true);
+          if (got) {
+            const float4 *from = reinterpret_cast<const float4 *>(red) + tid;
+            for (int c = split << shift; c < min((split + 1) << shift, mine); c += 4) {
+              float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < splits) {
+                  const float4 f = from[(((i << shift) + (c & ((1 << shift) - 1))) >> 2) * 128];
+                  sum = make_float4(sum.x + f.x, sum.y + f.y, sum.z + f.z, sum.w + f.w);
+                }
+              const uint64_t v[2] = {pair(__float_as_uint(sum.x), __float_as_uint(sum.y)),
+                                     pair(__float_as_uint(sum.z), __float_as_uint(sum.w))};
+              store_lanes<4>(P, base + c * P.ldo + lane, mine - c, lane < nl, lane & 1, v);
+            }
+          }
+          __syncwarp();
+          if (lane < splits) tc::arrive_at(tc::map_cta(red_empty, lane));
+          red_parity ^= 1;
+          return got;
+        };
         if constexpr (!G::F8) {
           if (nk > 0) {
             if (!(ok = warp_wait(&my_full[acc.at], acc.parity, P.status))) break;
             tc::fence_after();
           }
+          if constexpr (G::SPLIT) {
 #pragma unroll 1
-          for (int c = 0; c < mine; c += 32) {
-            uint32_t r[2][16];
-            if (nk > 0) {
-              ld_block(tmem + lane_addr + acc.at * G::BN + cw + c, r);
-              wait_block(r);
+            for (int c = 0; c < mine; c += 16) {
+              uint32_t r[16];
+              if (nk > 0) {
+                tc::ld16_nowait(tmem + lane_addr + acc.at * G::BN + c, r);
+                tc::wait_ld();
+                tie(r);
+              }
+              float v[16];  // a part without steps: zeros
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = nk > 0 ? __uint_as_float(r[i]) : 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) send(c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < mine; c += 32) {
+              uint32_t r[2][16];
+              if (nk > 0) {
+                ld_block(tmem + lane_addr + acc.at * G::BN + cw + c, r);
+                wait_block(r);
+              }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint64_t v[4];
+              for (int j = 0; j < 4; ++j) {
+                uint64_t v[4];
 #pragma unroll
-              for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
-                v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
-              store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
+                for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
+                  v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
+                store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
+              }
             }
           }
           if (nk > 0) release();
+          if constexpr (G::SPLIT) ok = join(base, nl);
         } else {
-          uint64_t v[G::COLS / 8][4];  // [8 columns][lane block]: two columns, folded by one packed FMA
+          uint64_t v[G::COLS / 2];  // pairs of neighbouring columns of this lane: one packed FMA folds both
 #pragma unroll
-          for (int i = 0; i < G::COLS / 8; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) v[i][g] = 0;
+          for (int i = 0; i < G::COLS / 2; ++i) v[i] = 0;
           // Scales of kScaleGroup blocks at a time, fetched while the group before is folded: thread tid has column
           // tid % 64 (the last one where there are fewer) of every other block.
           static_assert(G::F8 && G::COLS <= 64, "128 threads stage two blocks at a time");
-          const int tid = threadIdx.x & 127, col = tid & 63, odd = tid >> 6;
-          const float *xs = P.xs + t.row0 + t.c0 + min(col, mine - 1);
-          const float *ws = P.ws + ((long long)t.e * P.nOb + min((t.l0 + (int)rank * 128) / 128, P.nOb - 1)) * P.nKb;
+          const int col = tid & 63, odd = tid >> 6;
+          const float *xs = P.xs + k0 * P.ld_xs + t.row0 + t.c0 + min(col, mine - 1);
+          const float *ws = P.ws + ((long long)t.e * P.nOb + min((t.l0 + (int)rank * 128) / 128, P.nOb - 1)) * P.nKb + k0;
           float sx[kScaleGroup / 2], sw[kScaleGroup / 2];
           auto fetch = [&](int kb) {
 #pragma unroll
             for (int j = 0; j < kScaleGroup / 2; ++j) {
-              const int k = min(kb + 2 * j + odd, nk - 1);
+              const int k = max(min(kb + 2 * j + odd, nk - 1), 0);
               sx[j] = __ldg(xs + k * P.ld_xs);
               sw[j] = __ldg(ws + k);
             }
@@ -677,34 +791,38 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
             fetch(kg + kScaleGroup);
             // also keeps these warps within one group of each other: two buffers of scales do
             named_sync(1, 128);
-            sc += 2 * (lane & 3);
 #pragma unroll 1
             for (int kb = kg; kb < min(kg + kScaleGroup, nk); ++kb, sc += G::BN) {
               ok = ok && warp_wait(&my_full[acc.at], acc.parity, P.status);
               tc::fence_after();
               const uint32_t ta = tmem + lane_addr + acc.at * G::BN;
-              uint32_t r[2][2][8];
-              ld_block(ta, r[0]);
+              uint32_t r[2][16];
+              tc::ld16_nowait(ta, r[0]);
 #pragma unroll
               for (int c = 0; c < G::COLS / 16; ++c) {
                 if (16 * c < mine) {
-                  wait_block(r[c & 1]);
-                  if (c + 1 < G::COLS / 16 && 16 * (c + 1) < mine) ld_block(ta + 16 * (c + 1), r[(c + 1) & 1]);
+                  tc::wait_ld();
+                  tie(r[c & 1]);
+                  if (c + 1 < G::COLS / 16 && 16 * (c + 1) < mine) tc::ld16_nowait(ta + 16 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                  for (int j = 0; j < 2; ++j) {
-                    const uint64_t s = *reinterpret_cast<const uint64_t *>(sc + 16 * c + 8 * j);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                      fma2(v[2 * c + j][g], pair(r[c & 1][g >> 1][4 * j + 2 * (g & 1)], r[c & 1][g >> 1][4 * j + 2 * (g & 1) + 1]), s);
+                  for (int i = 0; i < 16; i += 4) {
+                    const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(sc + 16 * c + i);
+                    fma2(v[8 * c + i / 2], pair(r[c & 1][i], r[c & 1][i + 1]), s.x);
+                    fma2(v[8 * c + i / 2 + 1], pair(r[c & 1][i + 2], r[c & 1][i + 3]), s.y);
                   }
                 }
               }
               release();
             }
           }
+          if constexpr (G::SPLIT) {
 #pragma unroll
-          for (int j = 0; j < G::COLS / 8; ++j)
-            if (ok && 8 * j < mine) store_block(P, base + 8 * j * P.ldo, mine - 8 * j, nl, lane, v[j]);
+            for (int i = 0; i < G::COLS / 2; i += 2)
+              if (ok && 2 * i < mine) send(2 * i, low(v[i]), high(v[i]), low(v[i + 1]), high(v[i + 1]));
+          } else if (ok) {
+            store_lanes<G::COLS>(P, base + lane, mine, lane < nl, lane & 1, v);
+          }
+          if constexpr (G::SPLIT) ok = join(base, nl);
         }
       }
     }
@@ -713,6 +831,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  if constexpr (G::SPLIT) tc::cluster_sync();  // nothing may be sent to a CTA that has gone
   if constexpr (CG == 2) {
     // the last commit arrives in both CTAs; only here, where it is due, can a bounded wait for it start
     if (rank == 1 && warp == 1) warp_wait(drain, 0, P.status);
@@ -727,46 +846,88 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
 
 using Narrow = GCfg<1, 64, false>;
 using NarrowF8 = GCfg<1, 64, true>;
+using NarrowSplit = GCfg<1, 64, false, true>;
+using NarrowSplitF8 = GCfg<1, 64, true, true>;
 using Wide = GCfg<2, 256, false>;
 using WideF8 = GCfg<1, 256, true>;
 
+// The kernel, ready for a launch on the current device: one attribute call per instantiation and device.
 template <class G, GroupedMode MODE>
-cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
+cudaError_t configure() {
+  static std::atomic<uint64_t> configured{0};
   auto kern = grouped_kernel<G, MODE>;
-  static std::atomic<uint64_t> configured{0};  // one attribute call per instantiation and device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
-    if (e != cudaSuccess) return e;
-    if (G::SPLIT_REGS) {
-      // the split asks for no more registers than the block is launched with, or it would wait forever
-      cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-      if (fa.numRegs * G::THREADS < 128 * (kRegsControl + 2 * kRegsEpilogue)) return cudaErrorInvalidConfiguration;
-    }
-    configured.fetch_or(bit);
+  if (configured.load() & bit) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM)) != cudaSuccess) return e;
+  if (G::SPLIT_REGS) {
+    // the split asks for no more registers than the block is launched with, or it would wait forever
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs * G::THREADS < 128 * (kRegsControl + 2 * kRegsEpilogue)) return cudaErrorInvalidConfiguration;
   }
+  configured.fetch_or(bit);
+  return cudaSuccess;
+}
+
+// attr: room for two attributes
+template <class G>
+cudaLaunchConfig_t launch_config(int grid, int cluster, cudaLaunchAttribute *attr, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(G::THREADS);
   cfg.dynamicSmemBytes = G::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = G::CG;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = G::CG == 1 ? 1 : 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
+  cfg.numAttrs = cluster == 1 ? 1 : 2;
+  return cfg;
+}
+
+template <class G, GroupedMode MODE>
+cudaError_t launch_one(const GroupedArgs &a, int grid, cudaStream_t stream) {
+  cudaError_t e = configure<G, MODE>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = launch_config<G>(grid, G::SPLIT ? a.splits : G::CG, attr, stream);
+  e = cudaLaunchKernelEx(&cfg, grouped_kernel<G, MODE>, a);
   if (e != cudaSuccess) return e;
   count_launches();
   return cudaGetLastError();
+}
+
+// Asked once for each device and size; 0 where the question fails.
+template <class G, GroupedMode MODE>
+int clusters(int splits) {
+  static std::atomic<int> known[64][3];
+  const int which = splits == 2 ? 0 : splits == 4 ? 1 : 2;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  if ((n = known[dev][which].load()) > 0) return n - 1;
+  n = 0;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = launch_config<G>(splits, splits, attr, nullptr);
+  cfg.attrs = attr + 1;
+  cfg.numAttrs = 1;
+  if (configure<G, MODE>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, grouped_kernel<G, MODE>, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // not this call's failure: it runs without clusters
+    n = 0;
+  }
+  known[dev][which].store(n + 1);
+  return n;
+}
+
+template <GroupedMode MODE>
+cudaError_t launch_mode(const GroupedArgs &a, GroupedKernel k, int grid, cudaStream_t stream) {
+  if (k == GG_WIDE) return launch_one<Wide, MODE>(a, grid, stream);
+  return a.splits > 1 ? launch_one<NarrowSplit, MODE>(a, grid, stream) : launch_one<Narrow, MODE>(a, grid, stream);
 }
 
 }  // namespace
@@ -777,19 +938,24 @@ GroupedTile grouped_tile(GroupedKernel k, bool fp8) {
 }
 
 
+int grouped_clusters(GroupedMode mode, bool fp8, int splits) {
+  if (fp8) return clusters<NarrowSplitF8, GG_FWD>(splits);
+  return mode == GG_FWD ? clusters<NarrowSplit, GG_FWD>(splits)
+         : mode == GG_DX ? clusters<NarrowSplit, GG_DX>(splits)
+                         : clusters<NarrowSplit, GG_DW>(splits);
+}
+
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream) {
   if (fp8) {
     if (mode != GG_FWD) return cudaErrorInvalidValue;
-    return k == GG_WIDE ? launch_one<WideF8, GG_FWD>(a, grid, stream) : launch_one<NarrowF8, GG_FWD>(a, grid, stream);
+    if (k == GG_WIDE) return launch_one<WideF8, GG_FWD>(a, grid, stream);
+    return a.splits > 1 ? launch_one<NarrowSplitF8, GG_FWD>(a, grid, stream) : launch_one<NarrowF8, GG_FWD>(a, grid, stream);
   }
   switch (mode) {
-    case GG_FWD:
-      return k == GG_WIDE ? launch_one<Wide, GG_FWD>(a, grid, stream) : launch_one<Narrow, GG_FWD>(a, grid, stream);
-    case GG_DX:
-      return k == GG_WIDE ? launch_one<Wide, GG_DX>(a, grid, stream) : launch_one<Narrow, GG_DX>(a, grid, stream);
-    default:
-      return k == GG_WIDE ? launch_one<Wide, GG_DW>(a, grid, stream) : launch_one<Narrow, GG_DW>(a, grid, stream);
+    case GG_FWD: return launch_mode<GG_FWD>(a, k, grid, stream);
+    case GG_DX: return launch_mode<GG_DX>(a, k, grid, stream);
+    default: return launch_mode<GG_DW>(a, k, grid, stream);
   }
 }
 

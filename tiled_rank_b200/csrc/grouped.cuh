@@ -24,6 +24,7 @@ struct GroupedArgs {
   int L;                   // contiguous output dimension (wide fp8: not used)
   int C;                   // GG_DW: output rows per expert; wide fp8: the contiguous output dimension
   int R;                   // GG_FWD, GG_DX: reduction length
+  int splits;              // narrow kernel: CTAs that share a tile's reduction, 1, 2, 4 or 8
   int bf16;                // 16-bit operands: 1 bf16, 0 fp16
   void *out;
   int out_dtype;           // TILEQ_DT_*
@@ -45,6 +46,8 @@ struct GroupedTile {
   bool rows_on_lanes;
 };
 GroupedTile grouped_tile(GroupedKernel k, bool fp8);
+// Clusters of `splits` CTAs of the narrow kernel that the current device runs at the same time.
+int grouped_clusters(GroupedMode mode, bool fp8, int splits);
 // fp8 != 0: e4m3 operands with block scales (GG_FWD only).
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream);

@@ -101,6 +101,11 @@ __device__ __forceinline__ void arrive_expect_at(uint32_t cluster_addr, uint32_t
                "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void store4_at(uint32_t cluster_addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;\n" ::: "memory"); }
 // An arrival that orders tensor-memory reads only (after wait::ld and tcgen05.fence::before_thread_sync).
 __device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
