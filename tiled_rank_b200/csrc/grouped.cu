@@ -520,44 +520,45 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     }
   } else if (warp == 1 || (PARTS == 2 && warp == 2)) {
     // ============================================================ MMA issuer (one for each part)
-    // A stage costs a warp some 100 cycles for each barrier it asks and 200 to issue: with two accumulators a
-    // stage one warp would not keep the tensor core busy.
+    // (a stage costs the issuer some 350 cycles: with two accumulators a stage one would not keep the tensor core busy)
     if (rank == 0) {
       constexpr bool A_MN = MODE != GG_FWD, B_MN = MODE == GG_DW;  // output dimension contiguous
       const uint32_t fmt = P.bf16 && !G::F8 ? (1u << 7) | (1u << 10) : 0u;
       const int part = PARTS == 2 ? warp - 1 : 0;
       Ring<SQ> q;
       Ring<NACC> acc;
-      bool full_ready = false, acc_ready = false;
       const uint64_t ad0 = tc::sdesc(smem_addr(stage_a(0)), A_MN ? 8192 : 16);
       const uint64_t bd0 = tc::sdesc(smem_addr(stage_b(0)) + part * (G::PC / CG * 128), B_MN ? 8192 : 16);
-      for (int w = unit0; ok && tiles.get(w, t); w += units) {
-        const int nk = steps(t);
-        const bool mine = part < parts(t);
-        const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
-                               ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
-        const int k0 = first_step(nk), k1 = end_step(nk);
-        for (int kb = k0; kb < k1; ++kb, q.next()) {
-          const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
-          const bool last = G::F8 || kb == k1 - 1, first_k = G::F8 || kb == k0;
-          const int pa = part * NACC + acc.at;
-          // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
-          const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
-          const uint64_t at = (uint64_t)(q.at * (G::STAGE >> 4));
-          const bool want_acc = mine && first_k;
-          if (cut || !__all_sync(0xffffffffu, full_ready && (acc_ready || !want_acc)))
-            ok = warp_wait(&full[q.at], q.parity, P.status, cut) &&
-                 (!want_acc || warp_wait(&acc_empty[pa], acc.parity ^ 1, P.status));
-          if (!ok) break;
-          tc::fence_after();
-          // the next stage's barriers, asked now: the answers come while this one's MMAs are issued
-          const Ring<SQ> q1 = q.after();
-          full_ready = test_wait(&full[q1.at], q1.parity);
-          if (G::F8) {
-            const Ring<NACC> a1 = acc.after();
-            acc_ready = test_wait(&acc_empty[part * NACC + a1.at], a1.parity ^ 1);
-          }
-          if (tc::elect_one()) {
+      bool full_ready = false, acc_ready = false;
+      // One thread from here on: a stage then costs it some 350 cycles, against 470 for a warp that votes on every
+      // wait and elects for every issue.
+      if (tc::elect_one()) {
+        for (int w = unit0; ok && tiles.get(w, t); w += units) {
+          const int nk = steps(t);
+          const bool mine = part < parts(t);
+          const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+                                 ((uint32_t)(mma_n(t) >> 3) << 17) | ((uint32_t)(G::LANES >> 4) << 24);
+          const int k0 = first_step(nk), k1 = end_step(nk);
+          for (int kb = k0; kb < k1; ++kb, q.next()) {
+            const bool cut = MODE == GG_DW && kb == nk - 1 && (t.rows & 15);  // the producers zeroed rows
+            const bool last = G::F8 || kb == k1 - 1, first_k = G::F8 || kb == k0;
+            const int pa = part * NACC + acc.at;
+            // 16 (fp8: 32) reduction elements per MMA: 32 bytes along a row, or 16 rows
+            const int nmma = MODE == GG_DW ? min(4, (t.rows - kb * 64 + 15) / 16) : 4;
+            const uint64_t at = (uint64_t)(q.at * (G::STAGE >> 4));
+            const bool want_acc = mine && first_k;
+            if (cut || !full_ready)
+              ok = cut ? tc::mbar_wait_cluster(&full[q.at], q.parity, P.status) : mbar_wait(&full[q.at], q.parity, P.status);
+            if (ok && want_acc && !acc_ready) ok = mbar_wait(&acc_empty[pa], acc.parity ^ 1, P.status);
+            if (!ok) break;
+            tc::fence_after();
+            // the next stage's barriers, asked now: the answers come while this one's MMAs are issued
+            const Ring<SQ> q1 = q.after();
+            full_ready = test_wait(&full[q1.at], q1.parity);
+            if (G::F8) {  // (a part without columns in this tile leaves its ring where it is)
+              const Ring<NACC> a1 = acc.after();
+              acc_ready = mine && test_wait(&acc_empty[part * NACC + a1.at], a1.parity ^ 1);
+            }
             if (mine) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -567,15 +568,13 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
               if (last) tc::commit_cg<CG>(&acc_full[pa]);
             }
             tc::commit_cg<CG>(&empty[q.at]);
+            if (mine && last) acc.next();
           }
-          __syncwarp();
-          if (mine && last) acc.next();
         }
+        tc::commit_cg<CG>(drain);
       }
-      // all issued MMAs have retired before tensor memory is released
-      if (tc::elect_one()) tc::commit_cg<CG>(drain);
       __syncwarp();
-      warp_wait(drain, 0, P.status);
+      warp_wait(drain, 0, P.status);  // all issued MMAs have retired before tensor memory is released
     }
   } else if (warp == 3) {
     // ============================================================ rows of the next expert (GG_DW)
