@@ -234,6 +234,32 @@ def test_product_types_strides_and_other_rows(tq, out_dtype):
     assert y.dtype == dt
 
 
+def test_many_tiles_for_every_cta(tq):
+    """More tiles than CTAs in the wide kernel; the last column tile has one block of 128, another expert's a part."""
+    for O in (1408, 1300):
+        _check(tq, *_operands([700, 513, 0, 769, 300, 1025, 257, 640], 656, O, seed=O), f"many tiles {O}")
+
+
+def test_refusals(tq):
+    import torch
+    xq, xs, wq, ws, off = _operands([4, 4], 256, 160)
+    f = tq.fp8_gemm
+    for call in (lambda: f(xq.float(), xs, wq, ws, off), lambda: f(xq, xs.double(), wq, ws, off), lambda: f(xq, xs.t(), wq, ws, off),
+                 lambda: f(xq, xs[:1], wq, ws, off), lambda: f(xq, xs[:1].expand(2, 8), wq, ws, off), lambda: f(xq, xs, wq, ws[0], off),
+                 lambda: f(xq, xs, wq, ws[:, :1].expand(2, 2, 2), off), lambda: f(xq, xs, wq, ws), lambda: f(xq, xs, wq[0], ws[0], off),
+                 lambda: f(xq, xs, wq[:, :, :128], ws[:, :, :1], off), lambda: f(xq, xs, wq, ws, off, out_dtype=torch.float64),
+                 lambda: f(xq, xs, wq, ws, off, out=torch.empty(8, 159, dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    x = torch.zeros(8, 257, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: tq.fp8_quantize(x, swiglu=True), lambda: tq.fp8_quantize(x, rows=torch.zeros(4, dtype=torch.int64, device="cuda")),
+                 lambda: tq.fp8_quantize(x, row_scale=torch.zeros(7, device="cuda")), lambda: tq.fp8_quantize(x.to(torch.float64)),
+                 lambda: tq.fp8_quantize(x, out=torch.zeros(8, 257, device="cuda")), lambda: tq.fp8_quantize_weights(x[None, None]),
+                 lambda: tq.fp8_quantize_weights(x, scales=torch.zeros(1, 2, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_nan_row_and_nan_weight_block(tq):
     import torch
     xq, xs, wq, ws, off = _operands([20, 300], 384, 300, seed=2)

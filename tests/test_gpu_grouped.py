@@ -219,6 +219,77 @@ def test_other_streams_at_the_same_time(tq):
     assert all(torch.equal(o, want[i]) for i in (0, 1) for o in got[i])
 
 
+def test_many_tiles_for_every_cta(tq):
+    """More tiles than CTAs in the wide kernel, the last of each expert short in both directions."""
+    import torch
+    x, dy, w, off = _make([700, 513, 0, 769, 300, 1025, 257, 640], 712, 1416, torch.bfloat16, seed=3)
+    _check_all(tq, x, dy, w, off, "many tiles")
+
+
+def test_two_threads_and_two_graphs_at_once(tq):
+    import threading
+
+    import torch
+    data = [_make(c, 512, 768, torch.bfloat16, seed=i) for i, c in enumerate((LONG, RAGGED))]
+    want = [(tq.grouped_gemm(x, w, off), tq.grouped_gemm_dw(x, dy, off)) for x, dy, w, off in data]
+    torch.cuda.synchronize()
+    got, graphs = [None, None], []
+    for x, dy, w, off in data:
+        graph, out = torch.cuda.CUDAGraph(), (torch.zeros(x.shape[0], 768, dtype=x.dtype, device="cuda"), torch.zeros_like(w))
+        with torch.cuda.graph(graph):
+            tq.grouped_gemm(x, w, off, out=out[0])
+            tq.grouped_gemm_dw(x, dy, off, out=out[1])
+        graphs.append((graph, out))
+
+    def work(i):
+        x, dy, w, off = data[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[i] = [(tq.grouped_gemm(x, w, off), tq.grouped_gemm_dw(x, dy, off)) for _ in range(30)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in (0, 1):
+        assert all(torch.equal(a, want[i][0]) and torch.equal(b, want[i][1]) for a, b in got[i])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (graph, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, out), v in zip(graphs, want):
+        assert torch.equal(out[0], v[0]) and torch.equal(out[1], v[1])
+
+
+def test_refusals(tq):
+    """What does not fit raises before anything is launched, and the outputs stay as they were."""
+    import torch
+    x, dy, w, off = _make([4, 4], 64, 32, torch.bfloat16)
+    out = torch.full((8, 32), 5.0, dtype=x.dtype, device="cuda")
+    f = tq.grouped_gemm
+    for call in (lambda: f(x, w, off.long(), out=out), lambda: f(x, w, off[:2], out=out), lambda: f(x, w, off.cpu(), out=out),
+                 lambda: f(x, w.half(), off, out=out), lambda: f(x[:, :56], w, off, out=out), lambda: f(x, w[0], off, out=out),
+                 lambda: f(x, w.transpose(1, 2), off, out=out), lambda: f(x[:1].expand(8, 64), w, off, out=out),
+                 lambda: f(x, w[:1].expand(2, 32, 64), off, out=out), lambda: f(x, w, off, out=out[:7]),
+                 lambda: f(x, w, off, out=out.cpu()), lambda: f(x, w, off, out=out, out_dtype=torch.float32),
+                 lambda: f(x, w, off, out_dtype=torch.float64), lambda: f(x, w, off, out=out[:1].expand(8, 32)),
+                 lambda: f(x.t(), w, off, out=out), lambda: tq.grouped_gemm_dx(x, w, off),
+                 lambda: tq.grouped_gemm_dw(x, dy[:7], off), lambda: tq.grouped_gemm_dw(x, dy, off[:1]),
+                 lambda: tq.grouped_gemm_dw(x, dy, off, out=torch.empty(2, 64, 32, dtype=x.dtype, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    big = torch.zeros(8, 70, dtype=x.dtype, device="cuda")
+    for bad in (big[:, 1:65], big[:, :64]):          # not at 16 bytes; rows 140 bytes apart
+        with pytest.raises(tq.TileQError):
+            f(bad, w, off, out=out)
+    torch.cuda.synchronize()
+    assert (out == 5).all()
+
+
 def test_results_past_2_31_elements(tq):
     """Output offsets that do not fit 32 bits: 70000 x 32768 results, the last rows checked."""
     import torch
