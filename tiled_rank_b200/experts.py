@@ -32,6 +32,8 @@ ValueError before anything is launched.
 """
 from __future__ import annotations
 
+from ctypes import byref
+
 import torch
 
 from . import _lib as L
@@ -47,14 +49,21 @@ _status_words: dict = {}
 
 def _status_word(device: torch.device) -> torch.Tensor:
     """The device's status word, which the kernels write when a bounded wait gives up and never read."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("make one call outside of the graph first: it allocates the device's status word")
+    ws = torch.zeros(L.TILEQ_GROUPED_WS_BYTES, dtype=torch.uint8, device=device)
+    torch.cuda.current_stream(device).synchronize()  # zeroed before a call on any other stream
+    return _status_words.setdefault(device.index, ws)  # of two threads' words the first stays
+
+
+def _launch(function, device: torch.device, g, a, b, out, stream: int):
+    """A product's call: its operands, its result, the device's status word."""
     ws = _status_words.get(device.index)
     if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("make one call outside of the graph first: it allocates the device's status word")
-        ws = torch.zeros(L.TILEQ_GROUPED_WS_BYTES, dtype=torch.uint8, device=device)
-        torch.cuda.current_stream(device).synchronize()  # zeroed before a call on any other stream
-        _status_words[device.index] = ws
-    return ws
+        ws = _status_word(device)
+    status = function(byref(g), a.data_ptr(), b.data_ptr(), out.data_ptr(), ws.data_ptr(), L.TILEQ_GROUPED_WS_BYTES, stream)
+    if status:
+        raise L.TileQError(status, function.__name__)
 
 
 def expert_status(device="cuda") -> int:
@@ -64,14 +73,16 @@ def expert_status(device="cuda") -> int:
         device = torch.device(device.type, torch.cuda.current_device())
     with torch.cuda.device(device):
         torch.cuda.synchronize()
-        return L.tileq_device_status(_status_word(device))
+        ws = _status_words.get(device.index)
+        return L.tileq_device_status(_status_word(device) if ws is None else ws)
 
 
 def _on_stream(device: torch.device, stream, call):
     """call(raw stream) with `device` current, on `stream` or its current one; new outputs belong to that stream."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
     if stream is None:
+        index = device.index
+        if torch.cuda.current_device() == index:
+            return call(torch._C._cuda_getCurrentRawStream(index))
         stream = torch.cuda.current_stream(device)
     elif isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
@@ -120,7 +131,7 @@ def _vector(t, n: int, dtype, name: str, device) -> int:
     """Pointer of a contiguous vector of n values, 0 for none."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {device}")
     return t.data_ptr()
 
@@ -165,7 +176,7 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     def call(st):
         y = _result(out, out_dtype, x.dtype, (P, O), x)
         g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
-        L.tileq_grouped_gemm(g, x, w, y, _status_word(dev), st)
+        _launch(L.lib().tileq_grouped_gemm, dev, g, x, w, y, st)
         return y
     return _on_stream(dev, stream, call)
 
@@ -184,7 +195,7 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
     def call(st):
         dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
         g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, _rows(dx, "out")[2], ld_y, ld_w, stride_w, off)
-        L.tileq_grouped_gemm_dx(g, dy, w, dx, _status_word(dev), st)
+        _launch(L.lib().tileq_grouped_gemm_dx, dev, g, dy, w, dx, st)
         return dx
     return _on_stream(dev, stream, call)
 
@@ -206,7 +217,7 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
         dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
         ld_w, stride_w = _weights(dw, "out")[3:]
         g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
-        L.tileq_grouped_gemm_dw(g, x, dy, dw, _status_word(dev), st)
+        _launch(L.lib().tileq_grouped_gemm_dw, dev, g, x, dy, dw, st)
         return dw
     return _on_stream(dev, stream, call)
 
@@ -318,6 +329,7 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
     def call(st):
         y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
         g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
-        L.tileq_fp8_gemm(g, xq, xs, ld_xs, wq, ws, y, _status_word(dev), st)
+        word = _status_words.get(dev.index)
+        L.tileq_fp8_gemm(g, xq, xs, ld_xs, wq, ws, y, _status_word(dev) if word is None else word, st)
         return y
     return _on_stream(dev, stream, call)
