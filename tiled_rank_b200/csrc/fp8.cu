@@ -100,17 +100,22 @@ __device__ __forceinline__ uint32_t amax_pair(const Raw8<DT> &a, const Raw8<DT> 
   return __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
 }
 
-// Scale of a block from its maximum (top16), and the factor 1 / scale.  With amax = 1.m * 2^k and 448 = 1.75 * 2^8
-// the scale's exponent is k - 8, one more if 1.m > 1.75: 0x1f carries into the exponent just then.
-__device__ __forceinline__ float scale_of(uint32_t top, float &inv) {
+// Scale of a block from its maximum (top16).  With amax = 1.m * 2^k and 448 = 1.75 * 2^8 the scale's exponent is k - 8,
+// one more if 1.m > 1.75: 0x1f carries into the exponent just then.  1 for a block of zeros; a block with an infinity
+// or a NaN becomes NaN as a whole.
+__device__ __forceinline__ float scale_of(uint32_t top) {
   const int e = max((int)((top + 0x1fu) >> 7) - 8, 1);
-  inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  float s = __uint_as_float((uint32_t)e << 23);
-  if (top - 1u >= 0x7f7fu) {                    // zero, infinity or NaN
-    s = __uint_as_float(top ? 0x7fffffffu : 0x3f800000u);
-    if (top) inv = s;                           // the block becomes NaN as a whole
+  return __uint_as_float(top == 0 ? 0x3f800000u : top >= 0x7f80u ? 0x7fffffffu : (uint32_t)e << 23);
+}
+// The factors 1 / scale of two blocks from their maxima in the halves of m, as bf16 in the halves of the result.
+__device__ __forceinline__ uint32_t inverse_pair(uint32_t m) {
+  uint32_t e = ((m + 0x001f001fu) >> 7) & 0x01ff01ffu;
+  uint32_t inv = (0x01060106u - __vmaxu2(e, 0x00090009u)) << 7;  // biased exponent 254 - max(e - 8, 1)
+  if ((e + 0x00010001u) & 0x01000100u) {                         // e >= 255: near the top of the range, or beyond it
+    if ((m & 0xffffu) >= 0x7f80u) inv |= 0x7fffu;
+    if (m >> 16 >= 0x7f80u) inv |= 0x7fff0000u;
   }
-  return s;
+  return inv;
 }
 
 // Four fp32 values to e4m3 (nearest even, cut to +-448), in the order of memory.
@@ -126,13 +131,13 @@ __device__ __forceinline__ uint2 round8(const float (&v)[8], float inv) {
   return make_uint2(round4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     round4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
-// bf16 is scaled before it is widened (exact: a power of two; below bf16's normal range the result is zero in e4m3
-// either way).
+// Eight values as loaded; inv2: the factor as bf16 in both halves.  bf16 is scaled before it is widened (exact: a
+// power of two; below bf16's normal range the result is zero in e4m3 either way).
 template <int DT>
-__device__ __forceinline__ uint2 round8(const Raw8<DT> &r, float inv) {
+__device__ __forceinline__ uint2 round8(const Raw8<DT> &r, uint32_t inv2) {
   float v[8];
   if constexpr (DT == TILEQ_DT_BF16) {
-    const __nv_bfloat162 f = __float2bfloat162_rn(inv);
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&inv2);
     const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -144,7 +149,7 @@ __device__ __forceinline__ uint2 round8(const Raw8<DT> &r, float inv) {
     return make_uint2(round4(v[0], v[1], v[2], v[3]), round4(v[4], v[5], v[6], v[7]));
   } else {
     widen<DT>(r, v);
-    return round8(v, inv);
+    return round8(v, __uint_as_float(inv2 & 0xffff0000u));
   }
 }
 __device__ __forceinline__ void store_some(uint8_t *q, int n, uint2 w) {
@@ -176,7 +181,7 @@ constexpr int kQU = kQCols / 256;
 // FULL: all 1024 are there and aligned.
 template <int DT, QuantKind KIND, bool VEC, bool FULL>
 __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_t *q, int n, bool live, float factor,
-                                           float *sc, int lane) {
+                                           uint32_t *tops, int lane) {
   constexpr bool SWIGLU = KIND == Q_SWIGLU, PAIRS = KIND == Q_PLAIN && DT != TILEQ_DT_F32;
   constexpr int ES = DT == TILEQ_DT_F32 ? 4 : 2;
   Raw8<DT> raw[kQU], ups[SWIGLU ? kQU : 1];
@@ -227,17 +232,19 @@ __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_
     }
 #pragma unroll
     for (int d = 8; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if constexpr (PAIRS && DT == TILEQ_DT_F16)
+      m = top16(__float_as_uint(__half2float(__ushort_as_half((uint16_t)m)))) |
+          top16(__float_as_uint(__half2float(__ushort_as_half((uint16_t)(m >> 16))))) << 16;
+    if ((lane & 15) == 0) tops[(u + (lane >> 4)) * kQRows] = m;  // blocks 2 u and 2 u + 2, or those behind them
+    const uint32_t inv = inverse_pair(m);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t top = h ? m >> 16 : m & 0xffffu;
-      if constexpr (PAIRS && DT == TILEQ_DT_F16) top = top16(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))));
-      float inv;
-      const float s = scale_of(top, inv);
+      const uint32_t inv2 = __byte_perm(inv, 0, h ? 0x3232 : 0x1010);
       uint2 w;
       if constexpr (PAIRS)
-        w = round8<DT>(raw[u + h], inv);
+        w = round8<DT>(raw[u + h], inv2);
       else
-        w = round8(v[h], inv);
+        w = round8(v[h], __uint_as_float(inv2 & 0xffff0000u));
       uint8_t *to = q + (u + h) * 256;
       if constexpr (FULL) {
         *reinterpret_cast<uint2 *>(to) = w;
@@ -246,7 +253,6 @@ __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_
       } else {
         store_some(to, n - (u + h) * 256, w);
       }
-      if ((lane & 15) == 0) sc[((u + h) * 2 + (lane >> 4)) * kQRows] = s;
     }
   }
 }
@@ -258,9 +264,15 @@ __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_
 // The scales of eight rows leave together: neighbouring rows are neighbours in a scale row, and single 4-byte
 // stores would each cost a 32-byte sector.
 // VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
+// CTAs per SM: how many warps are there to cover the loads counts for more than a register or two.
+template <int DT, QuantKind KIND>
+constexpr int quant_ctas() {
+  return DT == TILEQ_DT_F32 ? (KIND == Q_SWIGLU ? 2 : 5) : KIND == Q_PLAIN ? 8 : KIND == Q_FACTOR ? 5 : 4;
+}
+
 template <int DT, QuantKind KIND, bool VEC>
-__global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRowsArgs P) {
-  __shared__ float sc[kQCols / 128][kQRows];
+__global__ void __launch_bounds__(kQRows * 32, quant_ctas<DT, KIND>()) quant_rows_kernel(const QuantRowsArgs P) {
+  __shared__ uint32_t tops[kQCols / 256][kQRows];  // two blocks' maxima each: blocks 4 i and 4 i + 2, or 4 i + 1 and 4 i + 3
   pdl_wait_and_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long r0 = (long long)blockIdx.x * kQRows, r = r0 + warp;
@@ -275,17 +287,18 @@ __global__ void __launch_bounds__(kQRows * 32) quant_rows_kernel(const QuantRows
     const float factor = KIND != Q_PLAIN && P.row_scale ? P.row_scale[r] : 1.f;
     if constexpr (VEC) {
       if (c0 + kQCols <= P.C)
-        quant_part<DT, KIND, true, true>(x, up, q, n, live, factor, &sc[0][warp], lane);
+        quant_part<DT, KIND, true, true>(x, up, q, n, live, factor, &tops[0][warp], lane);
       else
-        quant_part<DT, KIND, true, false>(x, up, q, n, live, factor, &sc[0][warp], lane);
+        quant_part<DT, KIND, true, false>(x, up, q, n, live, factor, &tops[0][warp], lane);
     } else {
-      quant_part<DT, KIND, false, false>(x, up, q, n, live, factor, &sc[0][warp], lane);
+      quant_part<DT, KIND, false, false>(x, up, q, n, live, factor, &tops[0][warp], lane);
     }
   }
   __syncthreads();
   if (threadIdx.x < kQCols / 128 * kQRows) {
     const int b = threadIdx.x / kQRows, i = threadIdx.x % kQRows;
-    if (c0 + b * 128 < P.C && r0 + i < P.R) P.scales[(c0 / 128 + b) * P.ld_s + r0 + i] = sc[b][i];
+    const uint32_t m = tops[(b >> 2) * 2 + (b & 1)][i];
+    if (c0 + b * 128 < P.C && r0 + i < P.R) P.scales[(c0 / 128 + b) * P.ld_s + r0 + i] = scale_of(b & 2 ? m >> 16 : m & 0xffffu);
   }
 }
 
@@ -324,8 +337,8 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, top[i]);
-  float inv;
-  const float s = scale_of(top16(m), inv);
+  const uint32_t t = top16(m);
+  const float inv = __uint_as_float(inverse_pair(t) << 16);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int o = o0 + 16 * i;
@@ -338,7 +351,7 @@ __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsAr
       }
     }
   }
-  if (threadIdx.x == 0) P.scales[blockIdx.x] = s;
+  if (threadIdx.x == 0) P.scales[blockIdx.x] = scale_of(t);
 }
 
 template <int DT, QuantKind KIND>
