@@ -40,62 +40,53 @@ from . import _lib as L
 
 _CODE = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16, torch.float32: L.TILEQ_DT_F32}
 _OPERAND = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16}
-_F8 = torch.float8_e4m3fn
-_status_words: dict = {}
+_I32, _F32, _F8 = torch.int32, torch.float32, torch.float8_e4m3fn
+_status_words: dict = {}   # of each device: the tensor and its address
 
 # A small product takes the GPU a few microseconds, so what a call costs on the host counts: the checks below read each
-# attribute once and build a message only when they raise.
+# attribute once, compare devices by number (-1: not on a GPU) and build a message only when they raise.
 
 
-def _status_word(device: torch.device) -> torch.Tensor:
+def _status_word(index: int):
     """The device's status word, which the kernels write when a bounded wait gives up and never read."""
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("make one call outside of the graph first: it allocates the device's status word")
-    ws = torch.zeros(L.TILEQ_GROUPED_WS_BYTES, dtype=torch.uint8, device=device)
-    torch.cuda.current_stream(device).synchronize()  # zeroed before a call on any other stream
-    return _status_words.setdefault(device.index, ws)  # of two threads' words the first stays
-
-
-def _launch(function, device: torch.device, g, a, b, out, stream: int):
-    """A product's call: its operands, its result, the device's status word."""
-    ws = _status_words.get(device.index)
-    if ws is None:
-        ws = _status_word(device)
-    status = function(byref(g), a.data_ptr(), b.data_ptr(), out.data_ptr(), ws.data_ptr(), L.TILEQ_GROUPED_WS_BYTES, stream)
-    if status:
-        raise L.TileQError(status, function.__name__)
+    ws = torch.zeros(L.TILEQ_GROUPED_WS_BYTES, dtype=torch.uint8, device=torch.device("cuda", index))
+    torch.cuda.current_stream(index).synchronize()  # zeroed before a call on any other stream
+    return _status_words.setdefault(index, (ws, ws.data_ptr()))  # of two threads' words the first stays
 
 
 def expert_status(device="cuda") -> int:
     """Synchronously read and clear the first device error of these calls (0: none), as tileq_device_status."""
     device = torch.device(device)
-    if device.index is None:
-        device = torch.device(device.type, torch.cuda.current_device())
-    with torch.cuda.device(device):
+    index = torch.cuda.current_device() if device.index is None else device.index
+    with torch.cuda.device(index):
         torch.cuda.synchronize()
-        ws = _status_words.get(device.index)
-        return L.tileq_device_status(_status_word(device) if ws is None else ws)
+        return L.tileq_device_status((_status_words.get(index) or _status_word(index))[0])
 
 
-def _on_stream(device: torch.device, stream, call):
-    """call(raw stream) with `device` current, on `stream` or its current one; new outputs belong to that stream."""
+def _elsewhere(index: int, stream, call):
+    """call() with device `index` and the given stream (or the device's own) current: where a call is not for the
+    current device's current stream.  New outputs belong to the stream they are made on."""
     if stream is None:
-        index = device.index
-        if torch.cuda.current_device() == index:
-            return call(torch._C._cuda_getCurrentRawStream(index))
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(index)
     elif isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", index))
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call()
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(rows, columns, row stride) of a matrix; the stride of a single row is 0, contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _check(status: int, name: str):
+    if status:
+        raise L.TileQError(status, name)
+
+
+def _rows(t: torch.Tensor, name: str, index: int):
+    """(rows, columns, row stride) of a matrix on device `index`; the stride of a single row is 0, contiguous."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}: all tensors must be on the same GPU")
     shape, stride = t.shape, t.stride()
     if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix, not of shape {tuple(shape)}")
@@ -111,10 +102,10 @@ def _rows(t: torch.Tensor, name: str):
     return n, c, stride[0]
 
 
-def _weights(t: torch.Tensor, name: str):
-    """(E, d_out, d_in, row stride, expert stride) of weights [E, d_out, d_in]."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _weights(t: torch.Tensor, name: str, index: int):
+    """(E, d_out, d_in, row stride, expert stride) of weights [E, d_out, d_in] on device `index`."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}: all tensors must be on the same GPU")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3:
         raise ValueError(f"{name} must be [E, d_out, d_in], not of shape {tuple(shape)}")
@@ -127,99 +118,97 @@ def _weights(t: torch.Tensor, name: str):
     return E, O, I, ld, (stride[0] if E > 1 else 0)
 
 
-def _vector(t, n: int, dtype, name: str, device) -> int:
+def _vector(t, n: int, dtype, name: str, index: int) -> int:
     """Pointer of a contiguous vector of n values, 0 for none."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {device}")
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on cuda:{index}")
     return t.data_ptr()
 
 
 def _result(out, out_dtype, default, shape, like: torch.Tensor) -> torch.Tensor:
     """The given result, checked, or a new one."""
     if out is None:
-        dtype = default if out_dtype is None else out_dtype
-        if dtype not in _CODE:
+        if out_dtype is None:
+            out_dtype = default
+        if out_dtype not in _CODE:
             raise ValueError("out_dtype must be bfloat16, float16 or float32")
-        return like.new_empty(shape) if dtype is like.dtype else torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape) if out_dtype is like.dtype else torch.empty(shape, dtype=out_dtype, device=like.device)
     if out.dtype not in _CODE or (out_dtype is not None and out.dtype is not out_dtype):
         raise ValueError("out must be bfloat16, float16 or float32, as out_dtype says")
-    if out.device != like.device or out.shape != shape:
-        raise ValueError(f"out must be of shape {tuple(shape)} on {like.device}")
+    if out.shape != shape:
+        raise ValueError(f"out must be of shape {tuple(shape)}")
     return out
 
 
-def _same(a: torch.Tensor, b: torch.Tensor, what: str):
-    if a.dtype is not b.dtype or a.device != b.device:
-        raise ValueError(f"{what} must have the same type and device")
-
-
-def _operand(t: torch.Tensor, name: str) -> int:
-    code = _OPERAND.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be bfloat16 or float16")
+def _operands(a: torch.Tensor, b: torch.Tensor) -> int:
+    """The type code of two 16-bit operands."""
+    dtype = a.dtype
+    code = _OPERAND.get(dtype)
+    if code is None or b.dtype is not dtype:
+        raise ValueError(f"the operands must both be bfloat16 or both float16, not {dtype} and {b.dtype}")
     return code
 
 
 def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """y [P, d_out] with y[p] = W_e x[p]: x [P, d_in], w [E, d_out, d_in]."""
-    code = _operand(x, "x")
-    P, I, ld_x = _rows(x, "x")
-    E, O, Iw, ld_w, stride_w = _weights(w, "w")
-    _same(x, w, "x and w")
+    code, index = _operands(x, w), x.get_device()
+    P, I, ld_x = _rows(x, "x", index)
+    E, O, Iw, ld_w, stride_w = _weights(w, "w", index)
     if I != Iw:
         raise ValueError(f"x has {I} columns, w expects {Iw}")
-    dev = x.device
-    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
-
-    def call(st):
-        y = _result(out, out_dtype, x.dtype, (P, O), x)
-        g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
-        _launch(L.lib().tileq_grouped_gemm, dev, g, x, w, y, st)
-        return y
-    return _on_stream(dev, stream, call)
+    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype))
+    y = _result(out, out_dtype, x.dtype, (P, O), x)
+    g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out", index)[2], ld_w, stride_w, off)
+    word = _status_words.get(index) or _status_word(index)
+    _check(L.lib().tileq_grouped_gemm(byref(g), x.data_ptr(), w.data_ptr(), y.data_ptr(), word[1], L.TILEQ_GROUPED_WS_BYTES,
+                                      torch._C._cuda_getCurrentRawStream(index)), "tileq_grouped_gemm")
+    return y
 
 
 def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """dx [P, d_in] with dx[p] = W_e^T dy[p]: dy [P, d_out], w [E, d_out, d_in]."""
-    code = _operand(dy, "dy")
-    P, O, ld_y = _rows(dy, "dy")
-    E, Ow, I, ld_w, stride_w = _weights(w, "w")
-    _same(dy, w, "dy and w")
+    code, index = _operands(dy, w), dy.get_device()
+    P, O, ld_y = _rows(dy, "dy", index)
+    E, Ow, I, ld_w, stride_w = _weights(w, "w", index)
     if O != Ow:
         raise ValueError(f"dy has {O} columns, w expects {Ow}")
-    dev = dy.device
-    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
-
-    def call(st):
-        dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
-        g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, _rows(dx, "out")[2], ld_y, ld_w, stride_w, off)
-        _launch(L.lib().tileq_grouped_gemm_dx, dev, g, dy, w, dx, st)
-        return dx
-    return _on_stream(dev, stream, call)
+    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype))
+    dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
+    g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, _rows(dx, "out", index)[2], ld_y, ld_w, stride_w, off)
+    word = _status_words.get(index) or _status_word(index)
+    _check(L.lib().tileq_grouped_gemm_dx(byref(g), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), word[1],
+                                         L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
+           "tileq_grouped_gemm_dx")
+    return dx
 
 
 def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None):
     """dW [E, d_out, d_in] with dW_e = sum over the rows p of e of dy[p] x[p]^T, zeros for an expert without rows."""
-    code = _operand(x, "x")
-    P, I, ld_x = _rows(x, "x")
-    Py, O, ld_y = _rows(dy, "dy")
-    _same(x, dy, "x and dy")
+    code, index = _operands(x, dy), x.get_device()
+    P, I, ld_x = _rows(x, "x", index)
+    Py, O, ld_y = _rows(dy, "dy", index)
     if P != Py:
         raise ValueError(f"x has {P} rows, dy {Py}")
-    dev, E = x.device, expert_offsets.numel() - 1
+    E = expert_offsets.numel() - 1
     if not 1 <= E <= L.TILEQ_GROUPED_MAX_E:
         raise ValueError(f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
-    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
-
-    def call(st):
-        dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
-        ld_w, stride_w = _weights(dw, "out")[3:]
-        g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
-        _launch(L.lib().tileq_grouped_gemm_dw, dev, g, x, dy, dw, st)
-        return dw
-    return _on_stream(dev, stream, call)
+    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype))
+    dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
+    ld_w, stride_w = _weights(dw, "out", index)[3:]
+    g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
+    word = _status_words.get(index) or _status_word(index)
+    _check(L.lib().tileq_grouped_gemm_dw(byref(g), x.data_ptr(), dy.data_ptr(), dw.data_ptr(), word[1],
+                                         L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
+           "tileq_grouped_gemm_dw")
+    return dw
 
 
 # ------------------------------------------------------------------ fp8
@@ -230,15 +219,15 @@ def _quantised(q, shape, like: torch.Tensor) -> torch.Tensor:
         if width % 16 == 0:
             return torch.empty(shape, dtype=_F8, device=like.device)
         return like.new_empty((*shape[:-1], -(-width // 16) * 16), dtype=_F8)[..., :width]
-    if q.dtype is not _F8 or q.device != like.device or q.shape != shape:
-        raise ValueError(f"out must be float8_e4m3fn of shape {tuple(shape)} on {like.device}")
+    if q.dtype is not _F8 or q.shape != shape:
+        raise ValueError(f"out must be float8_e4m3fn of shape {tuple(shape)}")
     return q
 
 
-def _scales(s, shape, device, name: str) -> int:
+def _scales(s, shape, index: int, name: str) -> int:
     """Row stride of a given scale tensor (0 where it has one row)."""
-    if s.dtype is not torch.float32 or s.device != device or s.shape != shape:
-        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on {device}")
+    if s.dtype is not _F32 or s.get_device() != index or s.shape != shape:
+        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on cuda:{index}")
     if len(shape) > 2:
         if not s.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -259,25 +248,26 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     code = _CODE.get(x.dtype)
     if code is None:
         raise ValueError("x must be bfloat16, float16 or float32")
-    T, C, ld_x = _rows(x, "x")
-    dev = x.device
+    index = x.get_device()
+    T, C, ld_x = _rows(x, "x", index)
     if swiglu:
         if C % 2:
             raise ValueError("x must hold the gate's and the up projection's columns")
         C //= 2
     R = T if rows is None else rows.numel()
-    at = _vector(rows, R, torch.int32, "rows", dev)
-    factor = _vector(row_scale, R, torch.float32, "row_scale", dev)
-    shape = (-(-C // 128), R)
-
-    def call(st):
-        q = _quantised(out, (R, C), x)
-        s = torch.empty(shape, dtype=torch.float32, device=dev) if scales is None else scales
-        ld_s = _scales(s, shape, dev, "scales")
-        a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out")[2], ld_s)
-        L.tileq_fp8_quantize(a, x, q, s, st)
-        return q, s
-    return _on_stream(dev, stream, call)
+    at = _vector(rows, R, _I32, "rows", index)
+    factor = _vector(row_scale, R, _F32, "row_scale", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        return _elsewhere(index, stream, lambda: fp8_quantize(x, rows, swiglu, row_scale, out, scales))
+    q, shape = _quantised(out, (R, C), x), (-(-C // 128), R)
+    if scales is None:
+        s, ld_s = torch.empty(shape, dtype=_F32, device=x.device), 0
+    else:
+        s, ld_s = scales, _scales(scales, shape, index, "scales")
+    a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out", index)[2], ld_s)
+    _check(L.lib().tileq_fp8_quantize(byref(a), x.data_ptr(), q.data_ptr(), s.data_ptr(),
+                                      torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize")
+    return q, s
 
 
 def fp8_quantize_weights(w, out=None, scales=None, stream=None):
@@ -290,18 +280,18 @@ def fp8_quantize_weights(w, out=None, scales=None, stream=None):
         q, s = fp8_quantize_weights(w[None], None if out is None else out[None], None if scales is None else scales[None],
                                     stream)
         return q[0], s[0]
-    E, O, I, ld_w, stride_w = _weights(w, "w")
-    dev, shape = w.device, (E, -(-O // 128), -(-I // 128))
-
-    def call(st):
-        q = _quantised(out, (E, O, I), w)
-        ld_q, stride_q = _weights(q, "out")[3:]
-        s = torch.empty(shape, dtype=torch.float32, device=dev) if scales is None else scales
-        _scales(s, shape, dev, "scales")
-        g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
-        L.tileq_fp8_quantize_weights(g, w, q, ld_q, stride_q, s, st)
-        return q, s
-    return _on_stream(dev, stream, call)
+    index = w.get_device()
+    E, O, I, ld_w, stride_w = _weights(w, "w", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        return _elsewhere(index, stream, lambda: fp8_quantize_weights(w, out, scales))
+    q, shape = _quantised(out, (E, O, I), w), (E, -(-O // 128), -(-I // 128))
+    ld_q, stride_q = _weights(q, "out", index)[3:]
+    s = torch.empty(shape, dtype=_F32, device=w.device) if scales is None else scales
+    _scales(s, shape, index, "scales")
+    g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
+    _check(L.lib().tileq_fp8_quantize_weights(byref(g), w.data_ptr(), q.data_ptr(), ld_q, stride_q, s.data_ptr(),
+                                              torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize_weights")
+    return q, s
 
 
 def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stream=None):
@@ -314,22 +304,25 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
         raise ValueError("a product by expert takes wq [E, d_out, d_in] and expert_offsets, a dense one wq [d_out, d_in]")
     if expert_offsets is None:
         wq, ws = wq[None], ws[None]
-    if xq.dtype is not _F8:
-        raise ValueError("xq must be float8_e4m3fn")
-    P, I, ld_x = _rows(xq, "xq")
-    E, O, Iw, ld_w, stride_w = _weights(wq, "wq")
-    _same(xq, wq, "xq and wq")
+    if xq.dtype is not _F8 or wq.dtype is not _F8:
+        raise ValueError("xq and wq must be float8_e4m3fn")
+    index = xq.get_device()
+    P, I, ld_x = _rows(xq, "xq", index)
+    E, O, Iw, ld_w, stride_w = _weights(wq, "wq", index)
     if I != Iw:
         raise ValueError(f"xq has {I} columns, wq expects {Iw}")
-    dev, kb = xq.device, -(-I // 128)
-    ld_xs = _scales(xs, (kb, P), dev, "xs")
-    _scales(ws, (E, -(-O // 128), kb), dev, "ws")
-    off = _vector(expert_offsets, E + 1, torch.int32, "expert_offsets", dev)
-
-    def call(st):
-        y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
-        g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out")[2], ld_w, stride_w, off)
-        word = _status_words.get(dev.index)
-        L.tileq_fp8_gemm(g, xq, xs, ld_xs, wq, ws, y, _status_word(dev) if word is None else word, st)
-        return y
-    return _on_stream(dev, stream, call)
+    kb = -(-I // 128)
+    ld_xs = _scales(xs, (kb, P), index, "xs")
+    _scales(ws, (E, -(-O // 128), kb), index, "ws")
+    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    if stream is not None or torch.cuda.current_device() != index:
+        if expert_offsets is None:
+            wq, ws = wq[0], ws[0]
+        return _elsewhere(index, stream, lambda: fp8_gemm(xq, xs, wq, ws, expert_offsets, out, out_dtype))
+    y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
+    g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out", index)[2], ld_w, stride_w, off)
+    word = _status_words.get(index) or _status_word(index)
+    _check(L.lib().tileq_fp8_gemm(byref(g), xq.data_ptr(), xs.data_ptr(), ld_xs, wq.data_ptr(), ws.data_ptr(), y.data_ptr(),
+                                  word[1], L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
+           "tileq_fp8_gemm")
+    return y
