@@ -215,51 +215,75 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Stores 8 columns (n of them exist) x 32 lanes (nl exist) to out + column * ldo + lane;
-// v[g]: this thread's two columns of lane 8 g + id / 4.  16-bit results are
-// transposed as 8 x 8 blocks, which leaves thread id the lanes 8 g + 2 (id % 4) + 0, 1
-// of column id / 4; WORDS is how much of them one store may take: 1 a value, 2 the
-// pair, 8 a run of eight lanes after a transposition among the four threads of a column.
-template <int DT, int WORDS>
-__device__ __forceinline__ void store_b16(uint16_t *out, long long ldo, int n, int nl, int id, const uint64_t (&v)[4]) {
-  uint32_t w[4];
+// Two values of neighbouring columns of a lane, rounded and transposed as 8 x 8 blocks: thread id, which had lane id / 4
+// of columns 2 (id % 4) + 0, 1, gets lanes 2 (id % 4) + 0, 1 of column id / 4.
+template <int DT>
+__device__ __forceinline__ uint32_t transpose8(uint32_t lo, uint32_t hi) {
+  uint32_t w;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n"
+               : "=r"(w)
+               : "r"(pack2<DT>(__uint_as_float(lo), __uint_as_float(hi))));
+  return w;
+}
+
+// Stores a block of 32 columns (n of them exist) x 32 lanes (nl exist, a multiple of 8) of 16-bit results in runs of
+// eight lanes, after a transposition among the four threads of a column.  The four groups of eight columns go through
+// each step together: one after the other, their latencies made this the most expensive part of a tile.
+template <int DT>
+__device__ __forceinline__ void store_runs(uint16_t *out, long long ldo, int n, int nl, int id, const uint32_t (&r)[2][16]) {
+  uint32_t w[4][4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(w[g]) : "r"(pack2<DT>(low(v[g]), high(v[g]))));
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) w[j][g] = transpose8<DT>(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]);
   const int q = id & 3;
+  const bool b0 = q & 1, b1 = q & 2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, b0 ? w[j][0] : w[j][1], 1);
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? w[j][2] : w[j][3], 1);
+    (b0 ? w[j][0] : w[j][1]) = x;
+    (b0 ? w[j][2] : w[j][3]) = y;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = __shfl_xor_sync(0xffffffffu, b1 ? w[j][0] : w[j][2], 2);
+    const uint32_t z = __shfl_xor_sync(0xffffffffu, b1 ? w[j][1] : w[j][3], 2);
+    (b1 ? w[j][0] : w[j][2]) = u;
+    (b1 ? w[j][1] : w[j][3]) = z;
+  }
+  out += (id >> 2) * ldo + q * 8;
+  n = q * 8 < nl ? n - (id >> 2) : 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j, out += 8 * ldo)
+    if (8 * j < n) *reinterpret_cast<uint4 *>(out) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+}
+
+// Stores 8 columns (n of them exist) x 32 lanes (nl exist) of 16-bit results to out + column * ldo + lane, one by one
+// or (PAIR) two neighbouring lanes at a time; v[g]: this thread's two columns of lane 8 g + id / 4.
+template <int DT, bool PAIR>
+__device__ __forceinline__ void store_b16(uint16_t *out, long long ldo, int n, int nl, int id, const uint64_t (&v)[4]) {
   out += (id >> 2) * ldo;
   const bool in = (id >> 2) < n;
-  if constexpr (WORDS == 8) {
-    const bool b0 = q & 1, b1 = q & 2;
-    const uint32_t x = __shfl_xor_sync(0xffffffffu, b0 ? w[0] : w[1], 1);
-    const uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? w[2] : w[3], 1);
-    const uint32_t a0 = b0 ? x : w[0], a1 = b0 ? w[1] : x, a2 = b0 ? y : w[2], a3 = b0 ? w[3] : y;
-    const uint32_t u = __shfl_xor_sync(0xffffffffu, b1 ? a0 : a2, 2);
-    const uint32_t z = __shfl_xor_sync(0xffffffffu, b1 ? a1 : a3, 2);
-    if (in && q * 8 < nl)
-      *reinterpret_cast<uint4 *>(out + q * 8) = b1 ? make_uint4(u, z, a2, a3) : make_uint4(a0, a1, u, z);
-  } else {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int l = 8 * g + 2 * q;
-      if constexpr (WORDS == 2) {
-        if (in && l < nl) *reinterpret_cast<uint32_t *>(out + l) = w[g];
-      } else {
-        if (in && l < nl) out[l] = (uint16_t)w[g];
-        if (in && l + 1 < nl) out[l + 1] = (uint16_t)(w[g] >> 16);
-      }
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t w = transpose8<DT>((uint32_t)v[g], (uint32_t)(v[g] >> 32));
+    const int l = 8 * g + 2 * (id & 3);
+    if constexpr (PAIR) {
+      if (in && l < nl) *reinterpret_cast<uint32_t *>(out + l) = w;
+    } else {
+      if (in && l < nl) out[l] = (uint16_t)w;
+      if (in && l + 1 < nl) out[l + 1] = (uint16_t)(w >> 16);
     }
   }
 }
 template <int DT>
 __device__ __forceinline__ void store_b16(const GroupedArgs &P, long long base, int n, int nl, int id, const uint64_t (&v)[4]) {
   uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base;
-  if (P.store_words >= 8)
-    store_b16<DT, 8>(out, P.ldo, n, nl, id, v);
-  else if (P.store_words == 2)
-    store_b16<DT, 2>(out, P.ldo, n, nl, id, v);
+  if (P.store_words == 2)
+    store_b16<DT, true>(out, P.ldo, n, nl, id, v);
   else
-    store_b16<DT, 1>(out, P.ldo, n, nl, id, v);
+    store_b16<DT, false>(out, P.ldo, n, nl, id, v);
 }
 __device__ __forceinline__ void store_block(const GroupedArgs &P, long long base, int n, int nl, int id, const uint64_t (&v)[4]) {
   if (P.out_dtype == TILEQ_DT_F32) {
@@ -420,8 +444,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc_cg<CG>(tmem_slot, G::TMEM_COLS);
-  // the prologue overlaps the previous kernel's tail
-  pdl_wait_and_release();
+  tc::grid_wait();  // the prologue overlaps the previous kernel's tail
   if (warp == 2) {
     // rows and tiles of each expert; offsets outside [0, P] are cut to it, one below its predecessor is raised to it
     int before = 0, top = P.offsets ? min(max(P.offsets[0], 0), P.P) : 0;
@@ -451,6 +474,8 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   __syncthreads();
   if constexpr (CG == 2 || G::SPLIT) tc::cluster_sync();
   tc::fence_after();
+  // only now: a kernel that starts early finds this one's tensor memory taken, not the other way round
+  tc::grid_release();
   const uint32_t tmem = *tmem_slot;
 
   auto steps = [&](const Tile &t) { return ((MODE == GG_DW ? t.rows : P.R) + G::KE - 1) / G::KE; };
@@ -743,20 +768,30 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
               for (int i = 0; i < 16; i += 4) send(c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           } else {
+            const bool runs = P.store_words >= 8 && P.out_dtype != TILEQ_DT_F32;
 #pragma unroll 1
             for (int c = 0; c < mine; c += 32) {
               uint32_t r[2][16];
               if (nk > 0) {
                 ld_block(tmem + lane_addr + acc.at * G::BN + cw + c, r);
                 wait_block(r);
+              } else {  // an expert without rows
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i >> 4][i & 15] = 0;
               }
+              uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + base + c * P.ldo;
+              if (runs && P.out_dtype == TILEQ_DT_BF16) {
+                store_runs<TILEQ_DT_BF16>(out, P.ldo, mine - c, nl, lane, r);
+              } else if (runs) {
+                store_runs<TILEQ_DT_F16>(out, P.ldo, mine - c, nl, lane, r);
+              } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint64_t v[4];
+                for (int j = 0; j < 4; ++j) {
+                  uint64_t v[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g)  // an expert without rows: zeros
-                  v[g] = nk > 0 ? pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]) : 0;
-                store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
+                  for (int g = 0; g < 4; ++g) v[g] = pair(r[g >> 1][4 * j + 2 * (g & 1)], r[g >> 1][4 * j + 2 * (g & 1) + 1]);
+                  store_block(P, base + (c + 8 * j) * P.ldo, mine - c - 8 * j, nl, lane, v);
+                }
               }
             }
           }
@@ -935,7 +970,6 @@ GroupedTile grouped_tile(GroupedKernel k, bool fp8) {
   if (k == GG_NARROW) return {Narrow::LANES, Narrow::BN, Narrow::BOX_B, false};
   return fp8 ? GroupedTile{WideF8::LANES, WideF8::BN, WideF8::BOX_B, true} : GroupedTile{Wide::LANES, Wide::BN, Wide::BOX_B, false};
 }
-
 
 int grouped_clusters(GroupedMode mode, bool fp8, int splits) {
   if (fp8) return clusters<NarrowSplitF8, GG_FWD>(splits);

@@ -75,6 +75,10 @@ __device__ __forceinline__ void commit_cg(uint64_t *bar) {
         : "memory");
 }
 
+// The two halves of pdl_wait_and_release.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 // ---------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
