@@ -353,7 +353,7 @@ tileq_status tileq_place_experts(const tileq_place_in *in, tileq_place_out *out,
  *   tileq_grouped_gemm_dw  dW_e  = sum over the rows p of expert e of dy[p] x[p]^T
  * Operands are bf16 or fp16, products are summed in fp32 and rounded once to
  * out_dtype.  Rows outside [expert_offsets[0], expert_offsets[E]) belong to no
- * expert: they are not read, and their output rows stay as they were.  dW is
+ * expert: their values do not matter, and their output rows stay as they were.  dW is
  * written for every expert (zeros where it has no rows).  Results are the same
  * bits on every run.
  *
@@ -376,7 +376,7 @@ typedef struct {
   int out_dtype;    /* result: TILEQ_DT_BF16, TILEQ_DT_F16 or TILEQ_DT_F32 */
   int E;            /* experts, 1..TILEQ_GROUPED_MAX_E */
   int P;            /* rows of x and y, >= 0 */
-  int d_in, d_out;  /* any widths >= 1 whose strides are allowed */
+  int d_in, d_out;  /* any widths >= 1 whose strides are allowed (they and P up to 2^31 - 2^16) */
   /* Strides in elements, 0 = contiguous: rows of x / dx (ld_x), of y / dy
    * (ld_y), rows and experts of W / dW [E, d_out, d_in] (ld_w, stride_w).
    * Those of operands (not of the result) must be multiples of 16 bytes, and no
@@ -398,7 +398,8 @@ tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const 
  * 128 x 128 block of W_e,
  *   y[p][o] = sum over blocks b of 128 inputs of
  *             xs[b][p] * ws[e][o / 128][b] * sum over i in b of xq[p][i] * wq[e][o][i]
- * summed in fp32 and rounded once to out_dtype.  The scales may have any value.
+ * summed in fp32 and rounded once to out_dtype.  The scales may have any value;
+ * xs * ws is formed first, in fp32.
  * A last block of fewer than 128 inputs or outputs has a scale like the others.
  *
  * The quantisers choose scale = the smallest power of two s with max|v| / s <=

@@ -68,6 +68,19 @@ def test_strides_a_tensor_map_cannot_have(L, name, bad):
     assert _call(L, name, **bad) == L.TILEQ_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("field", ["P", "d_in", "d_out"])
+def test_sizes_near_the_end_of_the_integers(L, name, field):
+    assert _call(L, name, **{field: (1 << 31) - 8}) == L.TILEQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("field", ["d_in", "d_out"])
+def test_weights_near_the_end_of_the_integers(L, field):
+    g = L.tileq_grouped(0, 0, 4, 0, 64, 128, 0, 0, 0, 0, None)
+    setattr(g, field, (1 << 31) - 8)
+    assert L.lib().tileq_fp8_quantize_weights(ctypes.byref(g), A16, A16, 0, 0, A16, None) == L.TILEQ_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name", CALLS[:2])
 def test_no_rows_enqueue_nothing(L, name):
     assert _call(L, name, P=0, a=None, out=None) == L.TILEQ_OK

@@ -29,6 +29,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// Rows and widths are rounded up to whole tiles in 32-bit integers.
+constexpr int kMostRows = 0x7fff0000;
+
 struct Operand {
   const void *base;
   int dtype;
@@ -95,6 +98,7 @@ tileq_status check(const tileq_grouped *g, const void *a, const void *b, const v
   if (!a || !b || !out || !aligned16(a) || !aligned16(b) || !aligned16(out)) return TILEQ_ERR_INVALID_ARG;
   if (!ws) return TILEQ_ERR_INVALID_ARG;
   if (ws_bytes < TILEQ_GROUPED_WS_BYTES) return TILEQ_ERR_WORKSPACE;
+  if (g->P > kMostRows || g->d_in > kMostRows || g->d_out > kMostRows) return TILEQ_ERR_UNSUPPORTED;
   return TILEQ_OK;
 }
 
@@ -304,6 +308,7 @@ tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, v
   };
   if (short_of(a.ld_w, a.stride_w) || short_of(a.ld_q, a.stride_q)) return TILEQ_ERR_INVALID_ARG;
   if (!w || !q || !scales || !aligned16(w) || !aligned16(q) || !aligned4(scales)) return TILEQ_ERR_INVALID_ARG;
+  if (g->d_in > kMostRows || g->d_out > kMostRows) return TILEQ_ERR_UNSUPPORTED;
   const int es = g->dtype == TILEQ_DT_F32 ? 4 : 2;
   a.w = w;
   a.q = static_cast<uint8_t *>(q);

@@ -26,9 +26,11 @@ the product is dense.
 Rows outside the offsets' range belong to no expert: a given ``out`` keeps them,
 a new one leaves them unset.  Calls are asynchronous on ``stream`` (the current
 stream of the tensors' device by default), hold no state from one to the next
-and can be captured into a CUDA graph.  Autograd does not record them: a backward
+and can be captured into a CUDA graph (after one call on that device outside of a
+graph, which allocates its status word).  Autograd does not record them: a backward
 pass calls the gradients' products itself.  Tensors that do not fit raise
-ValueError before anything is launched.
+ValueError, and TileQError what the library refuses (a stride or an address that is
+no multiple of 16 bytes), before anything is launched.
 """
 from __future__ import annotations
 
