@@ -118,11 +118,12 @@ long long tile_count(const GroupedTile &t, GroupedMode mode, const tileq_grouped
 //   dx  8 x 14336 -> 4096:   16 rows 145 / 139;   60 x 1408 -> 2048, 17 rows: 47.6 / 45.0
 //   fwd 1 x 2048 -> 2048:    256 rows (8 wide tiles) 12.9 / 15.9, 1024 rows (32) 22.7 / 16.7
 //   fp8 8 x 4096 -> 14336:   16 rows 91 / 97, 24 rows 101 / 97, 64 rows 161 / 102
-//   fp8 1 x 2048 -> 2048:    256 rows (16 wide tiles) 12.3 / 14.3, 1024 rows (64) 22.2 / 14.8
+//   fp8 1 x 8192 -> 1024:    512 rows (16 wide tiles) 21.1 / 27.6, 1024 rows (32) 32.3 / 27.9
+//   fp8 1 x 4096 -> 1536:    256 rows (12 wide tiles) 14.8 / 16.2, 512 rows (24) 18.5 / 16.5
 //   dW  512 x 512, 256 rows: 1 expert (4 wide tiles) 6.4 / 8.6, 60 experts (240) 31 / 21
 GroupedKernel pick(GroupedMode mode, const tileq_grouped *g, int contig, bool fp8) {
   const bool rows = mode == GG_DW || rows_per_expert(g) > (fp8 ? 12 : mode == GG_DX ? 6 : 16);
-  return rows && tile_count(grouped_tile(GG_WIDE, fp8), mode, g, contig) >= (fp8 ? 48 : 24) ? GG_WIDE : GG_NARROW;
+  return rows && tile_count(grouped_tile(GG_WIDE, fp8), mode, g, contig) >= 24 ? GG_WIDE : GG_NARROW;
 }
 
 // Where the narrow kernel has too few tiles for the GPU, clusters of CTAs share a tile's reduction, if it is long
