@@ -169,7 +169,7 @@ tileq_status run(GroupedArgs &a, GroupedMode mode, const tileq_grouped *g, const
   if (sms < 8) return TILEQ_ERR_CUDA;
   a.splits = k == GG_NARROW ? pick_splits(mode, g, tiles, a.R, fp8) : 1;
   const int group = cg * a.splits;
-  const int grid = (int)std::min<long long>(sms / group, on_lanes ? 2 * tiles : tiles) * group;  // (a CTA for each half tile)
+  const int grid = (int)std::min<long long>(sms / group, k == GG_WIDE ? 2 * tiles : tiles) * group;  // (wide: of half tiles)
   return launch_grouped(a, k, mode, fp8, grid, stream) == cudaSuccess ? TILEQ_OK : TILEQ_ERR_CUDA;
 }
 

@@ -76,6 +76,7 @@ struct GCfg {
   // ROWS: the columns of a tile are two MMAs, one for each 128 of d_out and so for each weight scale, with
   // accumulators of their own, folded by four epilogue warps each: while one part is folded the other's MMAs run
   static constexpr int PARTS = ROWS ? 2 : 1;
+  static constexpr bool HALVES = BN == 256;  // the tiles of a last round may be shared by two units
   static constexpr int PC = BN / PARTS;  // columns of a part
   static constexpr int BOX_B = ROWS ? PC / CG : BN == 256 ? 64 : 32;  // rows of a box of B where the reduction is contiguous
   static constexpr int NACC = BN == 256 ? 2 : 4;
@@ -118,14 +119,14 @@ __host__ __device__ __forceinline__ int tiles_of(int n, int size) { return (n + 
 template <class G, GroupedMode MODE>
 struct Tiles {
   const int *first, *beg;
-  int E, L, C, e = 0, halves = 0x7fffffff;  // halves: first tile that two CTAs share (ROWS)
+  int E, L, C, e = 0, halves = 0x7fffffff;  // halves: first tile that is shared by two (HALVES)
   // lanes and columns of an expert with `rows` rows
   __device__ int lanes(int rows) const { return G::ROWS ? rows : L; }
   __device__ int cols(int rows) const { return G::ROWS || MODE == GG_DW ? C : rows; }
   __device__ int count(int rows) const { return tiles_of(lanes(rows), G::LANES) * tiles_of(cols(rows), G::BN); }
   __device__ bool get(int w, Tile &t) {
     int half = -1;
-    if constexpr (G::ROWS) {
+    if constexpr (G::HALVES) {
       if (w >= halves) {
         half = (w - halves) & 1;
         w = halves + ((w - halves) >> 1);
@@ -135,20 +136,26 @@ struct Tiles {
     while (w >= first[e + 1]) ++e;
     const int i = w - first[e], rows = beg[e + 1] - beg[e], total = cols(rows);
     const int nl = tiles_of(lanes(rows), G::LANES), nc = tiles_of(total, G::BN);
-    const int grp = i / (kRowTileGroup * nl), rem = i - grp * kRowTileGroup * nl;
-    const int gsz = min(kRowTileGroup, nc - grp * kRowTileGroup);
-    const int l = rem / gsz, c = grp * kRowTileGroup + rem % gsz;
-    // equal tiles, rounded to the MMA's step: one short tile would leave its CTAs idle (ROWS: whole scale blocks)
-    const int step = G::ROWS ? G::BN : 16 * G::CG, tc = tiles_of(tiles_of(total, nc), step) * step;
+    const int step = G::ROWS ? G::BN : 16 * G::CG;  // (ROWS: whole scale blocks)
+    int l = i, c = 0, tc = tiles_of(total, step) * step;
+    if (nc > 1) {  // (divisions only where they are needed: every role waits for them at each tile)
+      const int grp = nc <= kRowTileGroup ? 0 : (uint32_t)i / (uint32_t)(kRowTileGroup * nl);
+      const int rem = i - grp * kRowTileGroup * nl, gsz = min(kRowTileGroup, nc - grp * kRowTileGroup);
+      l = (uint32_t)rem / (uint32_t)gsz;
+      c = grp * kRowTileGroup + rem - l * gsz;
+      // equal tiles, rounded to the MMA's step: one short tile would leave its CTAs idle
+      tc = G::ROWS ? step : tiles_of((uint32_t)(total + nc - 1) / (uint32_t)nc, step) * step;
+    }
     t.e = e;
     t.row0 = beg[e];
     t.rows = rows;
     t.l0 = l * G::LANES;
     t.c0 = c * tc;
     t.ncols = min(tc, total - t.c0);
-    if constexpr (G::ROWS) {
-      if (half == 0) t.ncols = min(t.ncols, G::PC);
-      if (half == 1) t.c0 += G::PC, t.ncols -= G::PC;
+    if constexpr (G::HALVES) {
+      const int h = G::ROWS ? G::PC : tiles_of(tiles_of(t.ncols, 2), step) * step;
+      if (half == 0) t.ncols = min(t.ncols, h);
+      if (half == 1) t.c0 += h, t.ncols -= h;  // none may be left
     }
     return true;
   }
@@ -488,10 +495,10 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   // only now: a kernel that starts early finds this one's tensor memory taken, not the other way round
   tc::grid_release();
   const uint32_t tmem = *tmem_slot;
-  if constexpr (G::ROWS) {
-    // Where the last round would leave half of the CTAs idle, each of its tiles is shared by two, a part each (the
-    // second has nothing to do where a tile has one part).  1 x 4096 -> 1536, 1024 rows: 21.0 -> 17.9 us.
-    const int rest = first[P.E] % units;
+  if constexpr (G::HALVES) {
+    // Where the last round would leave half of the GPU idle, two share each of its tiles, half of the columns each
+    // (ROWS: a part; the second has nothing to do where there is one).  fp8 1 x 4096 -> 1536, 1024 rows: 21.0 -> 17.2 us.
+    const int rest = (uint32_t)first[P.E] % (uint32_t)units;
     if (2 * rest <= units) tiles.halves = first[P.E] - rest;
   }
 
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     // ============================================================ producer
     Ring<SQ> q;
     for (int w = unit0; ok && tiles.get(w, t); w += units) {
-      if (G::ROWS && t.ncols <= 0) continue;
+      if (G::HALVES && t.ncols <= 0) continue;
       const int nk = steps(t), half = mma_n(t) / CG;
       const int l0 = t.l0 + (int)rank * 128, c0 = t.c0 + (int)rank * half;
       constexpr int ABOX = MODE == GG_FWD ? 1 : 2;           // boxes of A: 128 rows, or twice 64 columns
@@ -577,7 +584,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       // wait and elects for every issue.
       if (tc::elect_one()) {
         for (int w = unit0; ok && tiles.get(w, t); w += units) {
-          if (G::ROWS && t.ncols <= 0) continue;
+          if (G::HALVES && t.ncols <= 0) continue;
           const int nk = steps(t);
           const bool mine = part < parts(t);
           const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
@@ -626,6 +633,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     if constexpr (MODE == GG_DW) {
       uint32_t q0 = 0, phase = 0;  // phase: bit s, the use of tail[s]
       for (int w = unit0; ok && tiles.get(w, t); w += units) {
+        if (G::HALVES && t.ncols <= 0) continue;
         const int nk = steps(t), left = t.rows & 63;
         const int k0 = first_step(nk), k1 = end_step(nk);
         q0 += k1 - k0;
@@ -664,6 +672,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
     };
     // (narrow fp8: the four warps of a named barrier stay together, also after a wait that gave up)
     for (int w = unit0; (ok || G::F8) && tiles.get(w, t); w += units) {
+      if (G::HALVES && t.ncols <= 0) continue;
       const int steps_all = steps(t), k0 = first_step(steps_all), nk = end_step(steps_all) - k0;  // this CTA's steps
       const int l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
       const int cw = half * G::COLS;                  // first column of this warp
