@@ -675,8 +675,9 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
       if (G::HALVES && t.ncols <= 0) continue;
       const int steps_all = steps(t), k0 = first_step(steps_all), nk = end_step(steps_all) - k0;  // this CTA's steps
       const int l0 = t.l0 + (int)rank * 128 + (warp & 3) * 32;
-      const int cw = half * G::COLS;                  // first column of this warp
-      const int mine = min(t.ncols - cw, G::COLS);    // its columns, none if <= 0
+      // this warp's columns: of eight warps (but for ROWS) four have one half of the tile's, in blocks of 32
+      const int share = G::EPW == 8 && !G::ROWS ? tiles_of(t.ncols, 64) * 32 : G::COLS;
+      const int cw = half * share, mine = min(t.ncols - cw, share);  // first, and how many (none if <= 0)
       if constexpr (G::ROWS) {
         if (mine <= 0) continue;  // a part without columns has no MMAs either
         // this thread's row of x and y, and its scale with the part's weight scale, fetched two blocks ahead
