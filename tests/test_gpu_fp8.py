@@ -240,6 +240,13 @@ def test_many_tiles_for_every_cta(tq):
         _check(tq, *_operands([700, 513, 0, 769, 300, 1025, 257, 640], 656, O, seed=O), f"many tiles {O}")
 
 
+@pytest.mark.parametrize("counts", [[300], [600, 0, 290], [1024], [128, 140]])
+@pytest.mark.parametrize("I,O", [(512, 2048), (640, 1160), (2048, 640)])
+def test_shared_tiles_of_a_last_round(tq, counts, I, O):
+    """Few wide tiles: two CTAs share each, a part each; the second has nothing to do where d_out ends in the first."""
+    _check(tq, *_operands(counts, I, O), "shared")
+
+
 def test_refusals(tq):
     import torch
     xq, xs, wq, ws, off = _operands([4, 4], 256, 160)

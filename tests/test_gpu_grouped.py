@@ -265,6 +265,33 @@ def test_two_threads_and_two_graphs_at_once(tq):
         assert torch.equal(out[0], v[0]) and torch.equal(out[1], v[1])
 
 
+def test_a_first_call_in_a_capture_is_refused(tq, monkeypatch):
+    """The device's status word cannot be allocated there; a call before the capture makes it."""
+    import torch
+    from tiled_rank_b200 import experts
+    x, dy, w, off = _make([4, 4], 64, 32, torch.bfloat16)
+    with monkeypatch.context() as m:
+        m.setattr(experts, "_status_words", {})
+        with pytest.raises(RuntimeError, match="outside of the graph"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                tq.grouped_gemm(x, w, off)
+    want = tq.grouped_gemm(x, w, off)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = tq.grouped_gemm(x, w, off)
+    graph.replay()
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("counts", [[300], [600, 0, 290], [1024], [128, 140]])
+@pytest.mark.parametrize("d_in,d_out", [(512, 2048), (640, 1160), (2048, 640)])
+def test_shared_tiles_of_a_last_round(tq, counts, d_in, d_out):
+    """Few wide tiles: two pairs share each, an odd number of columns, or none, left for the second."""
+    import torch
+    x, dy, w, off = _make(counts, d_in, d_out, torch.bfloat16)
+    _check_all(tq, x, dy, w, off, "shared")
+
+
 def test_refusals(tq):
     """What does not fit raises before anything is launched, and the outputs stay as they were."""
     import torch

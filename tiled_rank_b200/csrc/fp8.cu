@@ -258,9 +258,10 @@ __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_
 }
 
 // One CTA per eight rows x 1024 columns, columns in the outer order: a slice of x that many rows are gathered from
-// stays in L2.  Gathered rows are then bound by instructions rather than by HBM, hence the 16-bit maxima and the
-// path for whole parts without any check.  (Persistent CTAs with the next item's loads in flight were slower, 276
-// against 195 us at 131072 x 4096: their registers leave a third of the warps.)
+// stays in L2.  131072 gathered bf16 rows of 4096: 168 us, 0.69 GB through HBM (63 % of measured) and 1.6 GB between L2
+// and the SMs, the ALUs at 78 %; hence the 16-bit maxima and the path for whole parts without any check.  8192 rows of
+// 28672 without a gather: 113 us, 6.3 TB/s.  (Persistent CTAs with the next item's loads in flight: 276 us against 195
+// for one item a CTA at the time, as their registers leave a third of the warps; a warp for eight rows: 175 against 168.)
 // The scales of eight rows leave together: neighbouring rows are neighbours in a scale row, and single 4-byte
 // stores would each cost a 32-byte sector.
 // VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kQRows * 32, quant_ctas<DT, KIND>()) quant_row
   }
 }
 
-// One CTA per 128 x 128 block, 64 values a thread.
+// One CTA per 128 x 128 block, 64 values a thread.  8 x 14336 x 4096 in bf16: 217 us, 6.5 TB/s.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsArgs P) {
   __shared__ uint32_t top[8];

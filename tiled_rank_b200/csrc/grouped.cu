@@ -20,10 +20,11 @@
 // half of B's, so an SM reads 32 KB per 64-element step of a 256 x 256 tile
 // instead of 48 KB).  Warps of a CTA:
 //   0      producer: TMA tiles (128-byte swizzle) of one 128-byte reduction step
-//          per stage into a ring;
-//   1      MMA issuer (first CTA of a pair): four MMAs per stage into an fp32
-//          TMEM accumulator, two or four accumulators in turn;
+//          per stage into a ring, a lane per box;
+//   1      MMA issuer (first CTA of a pair), one thread: four MMAs per stage into
+//          an fp32 TMEM accumulator, two or four accumulators in turn;
 //   2      the table of the experts' rows and tiles, before the others start;
+//          then, in wide fp8, the MMAs of the tile's second part;
 //   3      in GG_DW zeroes the rows of the next expert in the last stage of a
 //          tile (of both operands: 0 * NaN would be NaN);
 //   4..    epilogue: TMEM to registers, one rounding, stores.
@@ -36,7 +37,21 @@
 // there the operands change places: rows of x on the lanes (ROWS), each thread
 // with the scale of its own row in a register.
 // Few tiles, as of one expert's few rows: clusters of CTAs share the reduction of
-// each (SPLIT).
+// each (SPLIT); two units of the GPU share a tile of a last round (HALVES).
+//
+// What bounds them, measured on a B200 (of measured: of 6458 GB/s and 1663
+// TFLOP/s), the routing skewed as far as not said otherwise:
+//   one token on 8 experts, 4096 -> 14336    43 us    memory, 84 % of measured
+//   64 x 4096 -> 1536, 131072 rows           1.13 ms at full clocks, tensor cores,
+//                                            1460 TFLOP/s; 1.35 to 1.43 ms (1150 to
+//                                            1220) under the power limit
+//   gradient of 8192 rows, 60 experts        76 us    memory, 80 % of measured
+//   dW of 8192 rows, 8 x 14336 x 4096        0.72 ms at full clocks, 0.80 to 0.84 at the limit
+//   fp8, 64 x 4096 -> 1536, 128 rows         64 us    memory, 90 % of measured
+//   fp8, 8192 rows, 8 x 14336 -> 4096        0.46 ms at full clocks, 2080 TFLOP/s (even rows): the fold
+// The fold is why fp8 wide tiles stay at half of the tensor cores' rate: without
+// its FMAs a 2048 x 5632 x 2048 product took 25.5 us instead of 34.9, without its
+// TMEM reads 30.8.  (Pairs of CTAs and sixteen fold warps were no faster.)
 // Every wait is bounded and reports TILEQ_ERR_TIMEOUT.
 #include "grouped.cuh"
 
@@ -246,7 +261,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t lo, uint32_t hi) {
 
 // Stores a block of 32 columns (n of them exist) x 32 lanes (nl exist, a multiple of 8) of 16-bit results in runs of
 // eight lanes, after a transposition among the four threads of a column.  The four groups of eight columns go through
-// each step together: one after the other, their latencies made this the most expensive part of a tile.
+// each step together: one after the other, their latencies made this the most expensive part of a tile (dW of 512 rows,
+// 8 x 4096 x 1536: 48 us, together 31).
 template <int DT>
 __device__ __forceinline__ void store_runs(uint16_t *out, long long ldo, int n, int nl, int id, const uint32_t (&r)[2][16]) {
   uint32_t w[4][4];
