@@ -112,3 +112,37 @@ def test_training_step(tq, T, E, k, D, F):
     for name, v, leaf in zip(("gate", "up", "down", "x"), got, leaves):
         rel = ((v.double() - leaf.grad).norm() / leaf.grad.norm()).item()
         assert rel <= 6 * 2.0 ** -8, (name, rel)
+
+
+def test_bindings_of_the_library(tq):
+    """The calls as the C interface has them, structs filled by hand: the same results as on tensors."""
+    import torch
+    E, P, I, O = 3, 50, 160, 272
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    x, dy, w = rnd(P, I), rnd(P, O), rnd(E, O, I)
+    off = torch.tensor([0, 7, 7, P], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    call = tq.tileq_grouped(tq.TILEQ_DT_BF16, tq.TILEQ_DT_F32, E, P, I, O, 0, 0, 0, 0, off.data_ptr())
+    y, dx, dw = (torch.empty(*s, device="cuda") for s in ((P, O), (P, I), (E, O, I)))
+    tq.tileq_grouped_gemm(call, x, w, y, ws)
+    tq.tileq_grouped_gemm_dx(call, dy, w, dx, ws)
+    tq.tileq_grouped_gemm_dw(call, x, dy, dw, ws)
+    f32 = torch.float32
+    assert torch.equal(y, tq.grouped_gemm(x, w, off, out_dtype=f32))
+    assert torch.equal(dx, tq.grouped_gemm_dx(dy, w, off, out_dtype=f32))
+    assert torch.equal(dw, tq.grouped_gemm_dw(x, dy, off, out_dtype=f32))
+
+    f8 = torch.float8_e4m3fn
+    xq, xs = torch.empty(P, I, dtype=f8, device="cuda"), torch.empty(2, P, device="cuda")
+    wq, sw = torch.empty(E, O, I, dtype=f8, device="cuda"), torch.empty(E, 3, 2, device="cuda")
+    tq.tileq_fp8_quantize(tq.tileq_fp8_rows(tq.TILEQ_DT_BF16, P, P, I, 0, None, None, 0, 0, 0), x, xq, xs)
+    tq.tileq_fp8_quantize_weights(call, w, wq, 0, 0, sw)
+    call.dtype = tq.TILEQ_DT_E4M3
+    y8 = torch.empty(P, O, device="cuda")
+    tq.tileq_fp8_gemm(call, xq, xs, 0, wq, sw, y8, ws)
+    want = [*tq.fp8_quantize(x), *tq.fp8_quantize_weights(w)]
+    for a, b in zip((xq, xs, wq, sw), want):
+        assert torch.equal(a.float(), b.float())
+    assert torch.equal(y8, tq.fp8_gemm(*want, off, out_dtype=f32))
+    assert tq.tileq_device_status(ws) == 0

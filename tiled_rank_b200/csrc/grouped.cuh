@@ -48,7 +48,7 @@ struct GroupedTile {
 GroupedTile grouped_tile(GroupedKernel k, bool fp8);
 // Clusters of `splits` CTAs of the narrow kernel that the current device runs at the same time.
 int grouped_clusters(GroupedMode mode, bool fp8, int splits);
-// fp8 != 0: e4m3 operands with block scales (GG_FWD only).
+// fp8: e4m3 operands with block scales (GG_FWD only).
 cudaError_t launch_grouped(const GroupedArgs &a, GroupedKernel k, GroupedMode mode, bool fp8, int grid,
                            cudaStream_t stream);
 
