@@ -151,6 +151,16 @@ def test_widths_without_a_multiple_of_anything(tq):
         tq.grouped_gemm(rnd(1, I), rnd(1, 2, I), offsets_of([1], 0, "cuda"))
 
 
+@pytest.mark.parametrize("E", [1, 3])
+def test_experts_of_one_output(tq, E):
+    """A single row has no row stride that could be unfit."""
+    import torch
+    x, dy, w, off = _make([5] * E, 40, 1, torch.bfloat16)
+    wide = torch.zeros(5 * E, 8, dtype=x.dtype, device="cuda")
+    wide[:, :1] = dy
+    _check_all(tq, x[:, :37], wide[:, :1], w[:, :, :37], off, "one output")
+
+
 def test_no_rows(tq):
     import torch
     w = torch.ones(4, 24, 16, dtype=torch.bfloat16, device="cuda")

@@ -77,6 +77,7 @@ tileq_status strides_of(const tileq_grouped *g, int es, bool w_is_result, Stride
   if (s->x < g->d_in || s->y < g->d_out || s->w < g->d_in) return TILEQ_ERR_INVALID_ARG;
   s->we = g->stride_w ? g->stride_w : s->w * g->d_out;
   const long long matrix = (long long)(g->d_out - 1) * s->w + g->d_in;
+  if (g->d_out == 1) s->w = round_up(s->w, q);
   if (g->E == 1) s->we = round_up(std::max(s->we, matrix), q);
   if (s->we < matrix) return TILEQ_ERR_INVALID_ARG;
   // what a tensor map can express
