@@ -283,6 +283,11 @@ def test_dense(tq, P):
     import torch
     y = tq.fp8_gemm(xq, xs, wq[0], ws[0])
     assert torch.equal(y, _check(tq, xq, xs, wq, ws, off, "dense"))
+    one = _check(tq, xq, xs, wq[:, :1], ws[:, :1], off, "one output")
+    assert torch.equal(one, tq.fp8_gemm(xq, xs, wq[0, :1], ws[0, :1]))
+    for bad in ((wq[0], ws[0, :, :1]), (wq[0], ws[0].t().contiguous().t()), (wq[0, :0], ws[0, :0]), (wq[0, :, :512], ws[0, :, :4])):
+        with pytest.raises(ValueError):
+            tq.fp8_gemm(xq, xs, *bad)
 
 
 def test_no_rows(tq):

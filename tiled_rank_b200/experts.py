@@ -136,7 +136,7 @@ def _result(out, out_dtype, default, shape, like: torch.Tensor) -> torch.Tensor:
             out_dtype = default
         if out_dtype not in _CODE:
             raise ValueError("out_dtype must be bfloat16, float16 or float32")
-        return like.new_empty(shape) if out_dtype is like.dtype else torch.empty(shape, dtype=out_dtype, device=like.device)
+        return like.new_empty(shape) if out_dtype is like.dtype else like.new_empty(shape, dtype=out_dtype)
     if out.dtype not in _CODE or (out_dtype is not None and out.dtype is not out_dtype):
         raise ValueError("out must be bfloat16, float16 or float32, as out_dtype says")
     if out.shape != shape:
@@ -164,7 +164,8 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype))
     y = _result(out, out_dtype, x.dtype, (P, O), x)
-    g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out", index)[2], ld_w, stride_w, off)
+    ld_y = 0 if out is None else _rows(y, "out", index)[2]
+    g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
     word = _status_words.get(index) or _status_word(index)
     _check(L.lib().tileq_grouped_gemm(byref(g), x.data_ptr(), w.data_ptr(), y.data_ptr(), word[1], L.TILEQ_GROUPED_WS_BYTES,
                                       torch._C._cuda_getCurrentRawStream(index)), "tileq_grouped_gemm")
@@ -182,7 +183,8 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype))
     dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
-    g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, _rows(dx, "out", index)[2], ld_y, ld_w, stride_w, off)
+    ld_x = 0 if out is None else _rows(dx, "out", index)[2]
+    g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
     word = _status_words.get(index) or _status_word(index)
     _check(L.lib().tileq_grouped_gemm_dx(byref(g), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), word[1],
                                          L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
@@ -204,7 +206,7 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype))
     dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
-    ld_w, stride_w = _weights(dw, "out", index)[3:]
+    ld_w, stride_w = (0, 0) if out is None else _weights(dw, "out", index)[3:]
     g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
     word = _status_words.get(index) or _status_word(index)
     _check(L.lib().tileq_grouped_gemm_dw(byref(g), x.data_ptr(), dy.data_ptr(), dw.data_ptr(), word[1],
@@ -219,7 +221,7 @@ def _quantised(q, shape, like: torch.Tensor) -> torch.Tensor:
     if q is None:
         width = shape[-1]
         if width % 16 == 0:
-            return torch.empty(shape, dtype=_F8, device=like.device)
+            return like.new_empty(shape, dtype=_F8)
         return like.new_empty((*shape[:-1], -(-width // 16) * 16), dtype=_F8)[..., :width]
     if q.dtype is not _F8 or q.shape != shape:
         raise ValueError(f"out must be float8_e4m3fn of shape {tuple(shape)}")
@@ -263,7 +265,7 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
         return _elsewhere(index, stream, lambda: fp8_quantize(x, rows, swiglu, row_scale, out, scales))
     q, shape = _quantised(out, (R, C), x), (-(-C // 128), R)
     if scales is None:
-        s, ld_s = torch.empty(shape, dtype=_F32, device=x.device), 0
+        s, ld_s = x.new_empty(shape, dtype=_F32), 0
     else:
         s, ld_s = scales, _scales(scales, shape, index, "scales")
     a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out", index)[2], ld_s)
@@ -288,8 +290,11 @@ def fp8_quantize_weights(w, out=None, scales=None, stream=None):
         return _elsewhere(index, stream, lambda: fp8_quantize_weights(w, out, scales))
     q, shape = _quantised(out, (E, O, I), w), (E, -(-O // 128), -(-I // 128))
     ld_q, stride_q = _weights(q, "out", index)[3:]
-    s = torch.empty(shape, dtype=_F32, device=w.device) if scales is None else scales
-    _scales(s, shape, index, "scales")
+    if scales is None:
+        s = w.new_empty(shape, dtype=_F32)
+    else:
+        s = scales
+        _scales(s, shape, index, "scales")
     g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
     _check(L.lib().tileq_fp8_quantize_weights(byref(g), w.data_ptr(), q.data_ptr(), ld_q, stride_q, s.data_ptr(),
                                               torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize_weights")
@@ -304,25 +309,31 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
     """
     if (wq.dim() == 2) != (expert_offsets is None):
         raise ValueError("a product by expert takes wq [E, d_out, d_in] and expert_offsets, a dense one wq [d_out, d_in]")
-    if expert_offsets is None:
-        wq, ws = wq[None], ws[None]
     if xq.dtype is not _F8 or wq.dtype is not _F8:
         raise ValueError("xq and wq must be float8_e4m3fn")
     index = xq.get_device()
     P, I, ld_x = _rows(xq, "xq", index)
-    E, O, Iw, ld_w, stride_w = _weights(wq, "wq", index)
+    kb = -(-I // 128)
+    if expert_offsets is None:
+        O, Iw, ld_w = _rows(wq, "wq", index)
+        if O < 1:
+            raise ValueError("wq has no rows")
+        E, stride_w, blocks = 1, 0, (-(-O // 128), kb)
+    else:
+        E, O, Iw, ld_w, stride_w = _weights(wq, "wq", index)
+        blocks = (E, -(-O // 128), kb)
     if I != Iw:
         raise ValueError(f"xq has {I} columns, wq expects {Iw}")
-    kb = -(-I // 128)
     ld_xs = _scales(xs, (kb, P), index, "xs")
-    _scales(ws, (E, -(-O // 128), kb), index, "ws")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _scales(ws, blocks, index, "ws")
     off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
-        if expert_offsets is None:
-            wq, ws = wq[0], ws[0]
         return _elsewhere(index, stream, lambda: fp8_gemm(xq, xs, wq, ws, expert_offsets, out, out_dtype))
     y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
-    g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, _rows(y, "out", index)[2], ld_w, stride_w, off)
+    ld_y = 0 if out is None else _rows(y, "out", index)[2]
+    g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
     word = _status_words.get(index) or _status_word(index)
     _check(L.lib().tileq_fp8_gemm(byref(g), xq.data_ptr(), xs.data_ptr(), ld_xs, wq.data_ptr(), ws.data_ptr(), y.data_ptr(),
                                   word[1], L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
