@@ -363,3 +363,22 @@ def test_gradients_against_differences(tq):
     for num, ana, scale in (((f(x + vx, w) - f(x - vx, w)) / 2, (dx * vx.double()).sum(), (dx * vx.double()).norm()),
                             ((f(x, w + vw) - f(x, w - vw)) / 2, (dw * vw.double()).sum(), (dw * vw.double()).norm())):
         assert abs(num - ana) <= 1e-3 * scale, (num, ana, scale)
+
+
+def test_a_sum_that_takes_longer_than_a_second(tq):
+    """One expert of many with 450 million rows: its tile's reduction runs for more than a second, which no bounded wait
+    may take for a stop.  Rows of zeros but for three, whose products are small whole numbers."""
+    import torch
+    P, E, at = 450_000_000, 100, 40
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("20 GB of device memory")
+    x, dy = (torch.zeros(P, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n = torch.arange(1, 9, device="cuda", dtype=torch.bfloat16)
+    for i in (0, P // 2 + 5, P - 1):
+        x[i], dy[i] = 1, n
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[at + 1:] = P
+    dw = tq.grouped_gemm_dw(x, dy, off)
+    assert tq.expert_status() == 0
+    assert torch.equal(dw[at], (3 * n)[:, None].expand(8, 8))
+    assert (dw[:at] == 0).all() and (dw[at + 1:] == 0).all()

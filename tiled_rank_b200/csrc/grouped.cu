@@ -236,11 +236,16 @@ __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-// mbar_wait by a whole warp with one answer: no lane leaves a loop in which the others still meet.
+// A wait by a whole warp with one answer: no lane leaves a loop in which the others still meet.
 // (`remote`: the pair's other CTA has written memory before it arrived.)
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status, bool remote = false) {
-  return __all_sync(0xffffffffu, remote ? tc::mbar_wait_cluster(bar, parity, status) : mbar_wait(bar, parity, status));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status, bool remote = false,
+                                          long long limit = kWaitLimitCycles) {
+  return __all_sync(0xffffffffu,
+                    remote ? tc::mbar_wait_cluster(bar, parity, status, limit) : tc::mbar_wait_for(bar, parity, status, limit));
 }
+// The limit of a wait for the `steps` steps of a tile's reduction: a step takes some 500 cycles, so that a sum over 3e8
+// rows lasts longer than the second that suffices for a wait between neighbours in a pipeline.
+__device__ __forceinline__ long long reduction_limit(int steps) { return kWaitLimitCycles + 4096ll * steps; }
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -764,7 +769,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         int shift = 2;
         if constexpr (G::SPLIT) {
           while (splits << shift < t.ncols) ++shift;
-          ok = ok && warp_wait(red_empty, red_parity ^ 1, P.status, true);
+          ok = ok && warp_wait(red_empty, red_parity ^ 1, P.status, true, reduction_limit(steps_all));
         }
         [[maybe_unused]] const int tid = threadIdx.x & 127;
         [[maybe_unused]] auto send = [&](int c, float a, float b, float d, float e) {  // columns c .. c + 3 of this lane
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
           tc::fence_cluster();
           __syncwarp();
           if (lane < splits) tc::arrive_at(tc::map_cta(red_full, lane));
-          const bool got = ok && warp_wait(red_full, red_parity, P.status, true);
+          const bool got = ok && warp_wait(red_full, red_parity, P.status, true, reduction_limit(steps_all));
           if (got) {
             const float4 *from = reinterpret_cast<const float4 *>(red) + tid;
             for (int c = split << shift; c < min((split + 1) << shift, mine); c += 4) {
@@ -798,7 +803,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
         };
         if constexpr (!G::F8) {
           if (nk > 0) {
-            if (!(ok = warp_wait(&my_full[acc.at], acc.parity, P.status))) break;
+            if (!(ok = warp_wait(&my_full[acc.at], acc.parity, P.status, false, reduction_limit(nk)))) break;
             tc::fence_after();
           }
           if constexpr (G::SPLIT) {

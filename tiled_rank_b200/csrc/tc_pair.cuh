@@ -110,7 +110,19 @@ __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cl
 __device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
-// mbar_wait with cluster-scope acquire: the arrivals may come from another CTA.
+// mbar_wait with a limit of its own, for what takes longer than a step of a pipeline.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, int *status, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > limit) {
+      set_status(status, TILEQ_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+// The same with cluster-scope acquire: the arrivals may come from another CTA.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -121,11 +133,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, int *status) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, int *status,
+                                                  long long limit = kWaitLimitCycles) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait_cluster(bar, parity)) {
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       set_status(status, TILEQ_ERR_TIMEOUT);
       return false;
     }
