@@ -182,6 +182,29 @@ def test_tensors_that_do_not_fit():
     assert "grouped_gemm" in dir(tq)
 
 
+@pytest.mark.parametrize("call", ["grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw", "fp8_gemm"])
+def test_an_operand_that_requires_a_gradient(call):
+    """Autograd would lose it without a word: refused while gradients are enabled, before the tensors are looked at."""
+    torch = pytest.importorskip("torch")
+    import tiled_rank_b200 as tq
+    f8, off = torch.float8_e4m3fn, torch.zeros(3, dtype=torch.int32)
+    x, dy, w = torch.zeros(8, 64).bfloat16(), torch.zeros(8, 16).bfloat16(), torch.zeros(2, 16, 64).bfloat16()
+    xs, ws = torch.zeros(1, 8), torch.zeros(2, 1, 1)
+    args = {"grouped_gemm": (x, w, off), "grouped_gemm_dx": (dy, w, off), "grouped_gemm_dw": (x, dy, off),
+            "fp8_gemm": (x.to(f8), xs, w.to(f8), ws, off)}[call]
+    f = getattr(tq, call)
+    wants = [t for t in args if t.dtype in (torch.bfloat16, torch.float32)]
+    for t in wants:
+        t.requires_grad_()
+        with pytest.raises(ValueError, match="requires a gradient"):
+            f(*args)
+        with torch.no_grad(), pytest.raises(ValueError, match="on the same GPU"):
+            f(*args)
+        t.requires_grad_(False)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        f(*args, out=torch.zeros(8, 16, requires_grad=True))
+
+
 def test_the_package_imports_without_torch():
     """The binding needs torch only when a call is made with tensors."""
     code = ("import sys; sys.modules['torch'] = None; import tiled_rank_b200 as tq; "

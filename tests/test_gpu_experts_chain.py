@@ -114,6 +114,43 @@ def test_training_step(tq, T, E, k, D, F):
         assert rel <= 6 * 2.0 ** -8, (name, rel)
 
 
+def test_products_in_an_autograd_function(tq):
+    """The way to train through the products: refused in a recorded place, right in a Function, for a leaf that is used
+    twice.  The loss is the sum of y times a constant c that bf16 holds, so dy = c exactly and each gradient is one
+    product: a leaf's is within the product's bound, and of two uses within that of the sum rounded once more."""
+    import torch
+    from experts_util import bound, offsets_of, ref_dw, ref_dx
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    counts, I, O = [20, 0, 130, 50], 136, 72
+    off = offsets_of(counts, 0, "cuda")
+    x, w, c = rnd(sum(counts), I).requires_grad_(), rnd(4, O, I).requires_grad_(), rnd(sum(counts), O)
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, b):
+            ctx.save_for_backward(a, b)
+            return tq.grouped_gemm(a, b, off)
+
+        @staticmethod
+        def backward(ctx, dy):
+            a, b = ctx.saved_tensors
+            return tq.grouped_gemm_dx(dy, b, off), tq.grouped_gemm_dw(a, dy, off)
+
+    with pytest.raises(ValueError, match="requires a gradient"):
+        tq.grouped_gemm(x, w, off)
+    with torch.no_grad():
+        want = tq.grouped_gemm(x, w, off)
+    assert torch.equal(Product.apply(x, w), want)
+    for uses in (1, 2):
+        x.grad = w.grad = None
+        sum((Product.apply(x, w) * c).float().sum() for _ in range(uses)).backward()
+        for leaf, (ref, mag), terms in ((x, ref_dx(c, w.detach(), off), O), (w, ref_dw(x.detach(), c, off), max(counts))):
+            lim = uses * bound(leaf.dtype, ref, mag, terms)
+            lim = lim + (uses > 1) * (uses * ref.abs() + lim) * torch.finfo(leaf.dtype).eps / 2
+            assert ((leaf.grad.double() - uses * ref).abs() <= lim).all(), uses
+
+
 def test_bindings_of_the_library(tq):
     """The calls as the C interface has them, structs filled by hand: the same results as on tensors."""
     import torch

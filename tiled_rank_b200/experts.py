@@ -27,10 +27,15 @@ Rows outside the offsets' range belong to no expert: a given ``out`` keeps them,
 a new one leaves them unset.  Calls are asynchronous on ``stream`` (the current
 stream of the tensors' device by default), hold no state from one to the next
 and can be captured into a CUDA graph (after one call on that device outside of a
-graph, which allocates its status word).  Autograd does not record them: a backward
-pass calls the gradients' products itself.  Tensors that do not fit raise
-ValueError, and TileQError what the library refuses (a stride or an address that is
-no multiple of 16 bytes), before anything is launched.
+graph, which allocates its status word).
+
+Autograd does not record them: a backward pass calls the gradients' products itself.
+So that no gradient is lost unseen, a product with an operand that requires one raises
+ValueError while gradients are enabled: make it under ``torch.no_grad()`` or in a
+``torch.autograd.Function``.  (The quantisers take such tensors; their results are
+steps, without a gradient.)  Tensors that do not fit raise ValueError, and TileQError
+what the library refuses (a stride or an address that is no multiple of 16 bytes),
+before anything is launched.
 """
 from __future__ import annotations
 
@@ -83,6 +88,15 @@ def _elsewhere(index: int, stream, call):
 def _check(status: int, name: str):
     if status:
         raise L.TileQError(status, name)
+
+
+def _unrecorded(*tensors):
+    """No gradient may be lost silently: refuse what autograd would have to record."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("autograd does not record this product, and an operand requires a gradient: call it "
+                                 "under torch.no_grad() or in a torch.autograd.Function")
 
 
 def _rows(t: torch.Tensor, name: str, index: int):
@@ -155,6 +169,7 @@ def _operands(a: torch.Tensor, b: torch.Tensor) -> int:
 
 def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """y [P, d_out] with y[p] = W_e x[p]: x [P, d_in], w [E, d_out, d_in]."""
+    _unrecorded(x, w, out)
     code, index = _operands(x, w), x.get_device()
     P, I, ld_x = _rows(x, "x", index)
     E, O, Iw, ld_w, stride_w = _weights(w, "w", index)
@@ -174,6 +189,7 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
 
 def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """dx [P, d_in] with dx[p] = W_e^T dy[p]: dy [P, d_out], w [E, d_out, d_in]."""
+    _unrecorded(dy, w, out)
     code, index = _operands(dy, w), dy.get_device()
     P, O, ld_y = _rows(dy, "dy", index)
     E, Ow, I, ld_w, stride_w = _weights(w, "w", index)
@@ -194,6 +210,7 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
 
 def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None):
     """dW [E, d_out, d_in] with dW_e = sum over the rows p of e of dy[p] x[p]^T, zeros for an expert without rows."""
+    _unrecorded(x, dy, out)
     code, index = _operands(x, dy), x.get_device()
     P, I, ld_x = _rows(x, "x", index)
     Py, O, ld_y = _rows(dy, "dy", index)
@@ -307,6 +324,7 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
 
     Dense, without expert_offsets: wq [d_out, d_in], ws [ceil(d_out / 128), ceil(d_in / 128)].
     """
+    _unrecorded(xs, ws, out)
     if (wq.dim() == 2) != (expert_offsets is None):
         raise ValueError("a product by expert takes wq [E, d_out, d_in] and expert_offsets, a dense one wq [d_out, d_in]")
     if xq.dtype is not _F8 or wq.dtype is not _F8:
