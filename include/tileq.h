@@ -362,6 +362,10 @@ tileq_status tileq_place_experts(const tileq_place_in *in, tileq_place_out *out,
  * below its predecessor counts as equal to it, so no value of theirs leads out of
  * the arrays.
  *
+ * A result shares no byte with an operand, the offsets or the status word: tiles
+ * are written while others are still read (TILEQ_ERR_INVALID_ARG; columns of the
+ * same rows are not shared).
+ *
  * ws: device workspace of at least TILEQ_GROUPED_WS_BYTES, zeroed once by the
  * caller.  It holds the status word alone (tileq_device_status), which bounded
  * device waits that give up write; calls may share it, also at the same time.
@@ -420,7 +424,9 @@ typedef struct {
 } tileq_fp8_rows;
 
 /* q device e4m3 [R, C], scales device fp32 [ceil(C / 128), R] (all of a block
- * before the next).  Asynchronous; R == 0 enqueues nothing. */
+ * before the next); neither shares a byte with the other or with what is read
+ * (nor do the weights' and the product's results).  Asynchronous; R == 0 enqueues
+ * nothing. */
 tileq_status tileq_fp8_quantize(const tileq_fp8_rows *a, const void *x, void *q, float *scales,
                                 tileq_stream_t stream);
 

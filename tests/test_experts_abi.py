@@ -159,6 +159,84 @@ def test_fp8_quantize_weights_invalid(L, bad):
                                               None) == L.TILEQ_ERR_INVALID_ARG
 
 
+# ------------------------------------------------------------------ results over operands
+@pytest.mark.parametrize("name,over", [(n, over) for n in CALLS for over in (
+    dict(out=A16), dict(a=A16 + 32, out=A16), dict(b=A16 + (1 << 20)), dict(expert_offsets=A16 + (4 << 20) + 16),
+    dict(ws=A16 + (4 << 20) + 64))])
+def test_result_over_an_operand(L, name, over):
+    """The result lies over the first operand, its second row, the second operand, the offsets or the status word."""
+    apart = dict(a=A16, b=A16 + (1 << 20), out=A16 + (4 << 20), ws=A16 + (8 << 20), expert_offsets=A16 + (9 << 20))
+    if over == dict(b=A16 + (1 << 20)):
+        over = dict(out=apart["b"])
+    assert _call(L, name, **{**apart, **over}) == L.TILEQ_ERR_INVALID_ARG
+
+
+def test_fp8_results_over_operands(L):
+    big = [A16 + (i << 24) for i in range(1, 9)]
+    apart = dict(zip(("xq", "xs", "wq", "sw", "y", "ws", "expert_offsets"), big))
+    for k in ("xq", "xs", "wq", "sw", "ws", "expert_offsets"):
+        assert _fp8(L, **{**apart, "y": apart[k]}) == L.TILEQ_ERR_INVALID_ARG, k
+        assert _fp8(L, **{**apart, k: apart["y"] + 16}) == L.TILEQ_ERR_INVALID_ARG, k
+    apart = dict(zip(("x", "q", "s", "rows", "row_scale"), big))
+    for a, b in (("q", "x"), ("q", "s"), ("q", "rows"), ("q", "row_scale"), ("s", "x"), ("s", "rows"), ("s", "row_scale")):
+        assert _quant(L, **{**apart, a: apart[b]}) == L.TILEQ_ERR_INVALID_ARG, (a, b)
+        assert _quant(L, **{**apart, b: apart[a] + 16}) == L.TILEQ_ERR_INVALID_ARG, (a, b)
+    g = L.tileq_grouped(0, 0, 4, 0, 64, 128, 0, 0, 0, 0, None)
+    for w, q, s in ((0, 0, 1), (0, 1, 0), (1, 0, 0)):
+        assert L.lib().tileq_fp8_quantize_weights(ctypes.byref(g), big[w], big[q], 0, 0, big[s], None) == L.TILEQ_ERR_INVALID_ARG
+
+
+def test_shared_memory_against_every_byte(tmp_path):
+    """The host's test for a shared byte, over 200000 pairs of small arrays, against their bytes one by one."""
+    src = tmp_path / "share.cpp"
+    src.write_text(r'''
+#include <cstdio>
+#include <cstring>
+#include <random>
+#include "share.cuh"
+using namespace tileq;
+static char mem[8192];
+static void fill(const Memory &m, char *in) {
+  for (long long i = 0; i < m.mats; ++i)
+    for (long long r = 0; r < m.rows; ++r)
+      for (long long c = 0; c < m.width; ++c) in[(const char *)m.base - mem + i * m.stride + r * m.ld + c] = 1;
+}
+int main() {
+  std::mt19937 rng(1);
+  auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+  int yes = 0, no = 0;
+  for (int n = 0; n < 200000; ++n) {
+    Memory m[2];
+    const int same = pick(1, 40);
+    for (Memory &a : m) {
+      a.width = pick(1, 12);
+      a.rows = pick(0, 6);
+      a.ld = a.width + (pick(0, 2) ? pick(0, 30) : 0);
+      if (!pick(0, 1) && same >= a.width) a.ld = same;
+      a.mats = pick(0, 2) ? 1 : pick(1, 4);
+      a.stride = a.rows ? (a.rows - 1) * a.ld + a.width + pick(0, 60) : 0;
+      if (!pick(0, 1) && a.rows) a.stride = a.rows * a.ld;
+      a.base = mem + pick(0, 300);
+    }
+    static char x[8192], y[8192];
+    memset(x, 0, sizeof x), memset(y, 0, sizeof y);
+    fill(m[0], x), fill(m[1], y);
+    bool want = false;
+    for (int i = 0; i < 8192; ++i) want |= x[i] && y[i];
+    (want ? yes : no)++;
+    if (share(m[0], m[1]) != want || share(m[1], m[0]) != want) return std::printf("case %d: %d\n", n, want), 1;
+  }
+  std::printf("%d %d", yes, no);
+}
+''')
+    exe = tmp_path / "share"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "tiled_rank_b200", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
+    assert min(int(v) for v in run.stdout.split()) > 20000
+
+
 def test_tensors_that_do_not_fit():
     torch = pytest.importorskip("torch")
     import tiled_rank_b200 as tq

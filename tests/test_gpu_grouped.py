@@ -382,3 +382,42 @@ def test_a_sum_that_takes_longer_than_a_second(tq):
     assert tq.expert_status() == 0
     assert torch.equal(dw[at], (3 * n)[:, None].expand(8, 8))
     assert (dw[:at] == 0).all() and (dw[at + 1:] == 0).all()
+
+
+def test_results_beside_and_over_operands(tq):
+    """Columns of the operands' own rows, the room between them and memory right behind them take a result; a shared
+    byte is refused."""
+    import torch
+    counts, I, O = [40, 0, 3, 170], 64, 48
+    x, dy, w, off = _make(counts, I, O, torch.bfloat16, seed=21)
+    P, E = sum(counts), len(counts)
+    want, wdx, wdw = tq.grouped_gemm(x, w, off), tq.grouped_gemm_dx(dy, w, off), tq.grouped_gemm_dw(x, dy, off)
+    both = torch.zeros(P, I + O, dtype=x.dtype, device="cuda")
+    both[:, :I] = x
+    assert torch.equal(tq.grouped_gemm(both[:, :I], w, off, out=both[:, I:]), want) and torch.equal(both[:, :I], x)
+    one = torch.zeros(P * (I + O), dtype=x.dtype, device="cuda")
+    a, b = one[:P * I].view(P, I), one[P * I:].view(P, O)
+    assert torch.equal(tq.grouped_gemm(a.copy_(x), w, off, out=b), want)
+    # a gradient in the columns behind the rows' and behind every matrix of the weights
+    rows = torch.zeros(P, O + I, dtype=x.dtype, device="cuda")
+    rows[:, :O] = dy
+    assert torch.equal(tq.grouped_gemm_dx(rows[:, :O], w, off, out=rows[:, O:]), wdx)
+    pair = torch.zeros(E, 2, O, I, dtype=x.dtype, device="cuda")
+    pair[:, 0] = w
+    assert torch.equal(tq.grouped_gemm(x, pair[:, 0], off), want)
+    assert torch.equal(tq.grouped_gemm_dw(x, dy, off, out=pair[:, 1]), wdw) and torch.equal(pair[:, 0], w)
+    # results in the gaps of rows of another length
+    gaps = torch.zeros(64 * P, dtype=x.dtype, device="cuda")
+    xs, ys = gaps.view(P, 64)[:, :16], gaps.view(P // 3, 192)[:, 16:64]
+    few = offsets_of([P // 3], 0, "cuda")
+    w1 = w[:1, :, :16].contiguous()
+    assert torch.equal(tq.grouped_gemm(xs.copy_(x[:, :16])[:P // 3], w1, few, out=ys),
+                       tq.grouped_gemm(x[:P // 3, :16].contiguous(), w1, few))
+    square = torch.randn(E, I, I, device="cuda").to(x.dtype)
+    keep = x.clone()
+    for call in (lambda: tq.grouped_gemm(x, square, off, out=x), lambda: tq.grouped_gemm_dx(x, square, off, out=x),
+                 lambda: tq.grouped_gemm(both[:, :I], w, off, out=both[:, I - 8:I + O - 8]),
+                 lambda: tq.grouped_gemm_dw(x, x[:, :8], off, out=x.view(-1)[:E * 8 * I].view(E, 8, I))):
+        with pytest.raises(tq.TileQError):
+            call()
+    assert torch.equal(x, keep)

@@ -8,6 +8,7 @@
 #include "fp8.cuh"
 #include "grouped.cuh"
 #include "kernels.cuh"
+#include "share.cuh"
 
 namespace tileq {
 namespace {
@@ -54,6 +55,12 @@ bool encode(CUtensorMap *m, const Operand &o, int box_rows) {
   return fn(m, type, 3, const_cast<void *>(o.base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int element_size(int dtype) { return dtype == TILEQ_DT_F32 ? 4 : dtype == TILEQ_DT_E4M3 ? 1 : 2; }
+// The offsets and the status word, which no result may overwrite.
+bool share_control(const tileq_grouped *g, const void *ws, const Memory &out) {
+  return share(out, {g->expert_offsets, 4ll * (g->E + 1)}) || share(out, {ws, TILEQ_GROUPED_WS_BYTES});
 }
 
 int sm_count() {
@@ -190,6 +197,11 @@ tileq_status tileq_grouped_gemm(const tileq_grouped *g, const void *x, const voi
   if ((st = strides_of(g, 2, false, &s)) != TILEQ_OK) return st;
   if (s.x % 8 || s.w % 8 || s.we % 8) return TILEQ_ERR_UNSUPPORTED;
   if (g->P == 0) return TILEQ_OK;
+  const long long eo = element_size(g->out_dtype);
+  const Memory out = {y, g->d_out * eo, g->P, s.y * eo};
+  if (share(out, {x, g->d_in * 2ll, g->P, s.x * 2}) || share(out, {w, g->d_in * 2ll, g->d_out, s.w * 2, g->E, s.we * 2}) ||
+      share_control(g, ws, out))
+    return TILEQ_ERR_INVALID_ARG;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
   a.R = g->d_in;
@@ -209,6 +221,11 @@ tileq_status tileq_grouped_gemm_dx(const tileq_grouped *g, const void *dy, const
   if ((st = strides_of(g, 2, false, &s)) != TILEQ_OK) return st;
   if (s.y % 8 || s.w % 8 || s.we % 8) return TILEQ_ERR_UNSUPPORTED;
   if (g->P == 0) return TILEQ_OK;
+  const long long eo = element_size(g->out_dtype);
+  const Memory out = {dx, g->d_in * eo, g->P, s.x * eo};
+  if (share(out, {dy, g->d_out * 2ll, g->P, s.y * 2}) || share(out, {w, g->d_in * 2ll, g->d_out, s.w * 2, g->E, s.we * 2}) ||
+      share_control(g, ws, out))
+    return TILEQ_ERR_INVALID_ARG;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
   a.R = g->d_out;
@@ -227,6 +244,11 @@ tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const 
   Strides s;
   if ((st = strides_of(g, 2, true, &s)) != TILEQ_OK) return st;
   if (s.x % 8 || s.y % 8) return TILEQ_ERR_UNSUPPORTED;
+  const long long eo = element_size(g->out_dtype);
+  const Memory out = {dw, g->d_in * eo, g->d_out, s.w * eo, g->E, s.we * eo};
+  if (share(out, {x, g->d_in * 2ll, g->P, s.x * 2}) || share(out, {dy, g->d_out * 2ll, g->P, s.y * 2}) ||
+      share_control(g, ws, out))
+    return TILEQ_ERR_INVALID_ARG;
   GroupedArgs a;
   std::memset(&a, 0, sizeof(a));
   a.out = dw;
@@ -258,6 +280,12 @@ tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float 
   a.ld_xs = ld_xs ? ld_xs : g->P;
   a.nOb = (int)div_up(g->d_out, 128);
   a.nKb = (int)div_up(g->d_in, 128);
+  const long long eo = element_size(g->out_dtype);
+  const Memory out = {y, g->d_out * eo, g->P, s.y * eo};
+  if (share(out, {xq, g->d_in, g->P, s.x}) || share(out, {wq, g->d_in, g->d_out, s.w, g->E, s.we}) ||
+      share(out, {xs, 4ll * g->P, a.nKb, 4 * a.ld_xs}) || share(out, {w_scales, 4ll * g->E * a.nOb * a.nKb}) ||
+      share_control(g, ws, out))
+    return TILEQ_ERR_INVALID_ARG;
   a.status = static_cast<int *>(ws);
   return run(a, GG_FWD, g, {wq, TILEQ_DT_E4M3, g->d_in, g->d_out, g->E, s.w, s.we},
              {xq, TILEQ_DT_E4M3, g->d_in, g->P, 0, s.x, 0}, g->d_out, true, reinterpret_cast<cudaStream_t>(stream));
@@ -275,7 +303,13 @@ tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q,
   if (p->R == 0) return TILEQ_OK;
   if (!q || !scales || !aligned16(q) || !aligned4(scales) || (!x && p->T > 0) || !aligned16(x)) return TILEQ_ERR_INVALID_ARG;
   if (div_up(p->C, 1024) > 65535) return TILEQ_ERR_UNSUPPORTED;
-  const int es = p->dtype == TILEQ_DT_F32 ? 4 : 2;
+  const int es = element_size(p->dtype);
+  const Memory to = {q, p->C, p->R, p->R > 1 ? ld_q : 0}, to_scales = {scales, 4ll * p->R, div_up(p->C, 128), 4 * ld_s};
+  const Memory from = {x, width * es, p->T, p->T > 1 ? ld_x * es : 0};
+  const Memory of_rows[2] = {{p->rows, 4ll * p->R}, {p->row_scale, 4ll * p->R}};
+  if (share(to, to_scales) || share(to, from) || share(to_scales, from)) return TILEQ_ERR_INVALID_ARG;
+  for (const Memory &m : of_rows)
+    if (share(to, m) || share(to_scales, m)) return TILEQ_ERR_INVALID_ARG;
   QuantRowsArgs a;
   a.x = x;
   a.rows = p->rows;
@@ -311,7 +345,7 @@ tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, v
   if (short_of(a.ld_w, a.stride_w) || short_of(a.ld_q, a.stride_q)) return TILEQ_ERR_INVALID_ARG;
   if (!w || !q || !scales || !aligned16(w) || !aligned16(q) || !aligned4(scales)) return TILEQ_ERR_INVALID_ARG;
   if (g->d_in > kMostRows || g->d_out > kMostRows) return TILEQ_ERR_UNSUPPORTED;
-  const int es = g->dtype == TILEQ_DT_F32 ? 4 : 2;
+  const int es = element_size(g->dtype);
   a.w = w;
   a.q = static_cast<uint8_t *>(q);
   a.scales = scales;
@@ -324,6 +358,9 @@ tileq_status tileq_fp8_quantize_weights(const tileq_grouped *g, const void *w, v
           (g->E == 1 || (a.stride_w * es % 16 == 0 && a.stride_q % 8 == 0));
   const long long blocks = (long long)g->E * a.nO * a.nI;
   if (blocks > 0x7fffffff) return TILEQ_ERR_UNSUPPORTED;
+  const Memory to = {q, g->d_in, g->d_out, a.ld_q, g->E, a.stride_q}, to_scales = {scales, 4 * blocks};
+  const Memory from = {w, (long long)g->d_in * es, g->d_out, a.ld_w * es, g->E, a.stride_w * es};
+  if (share(to, to_scales) || share(to, from) || share(to_scales, from)) return TILEQ_ERR_INVALID_ARG;
   return launch_quant_weights(a, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILEQ_OK
                                                                                                     : TILEQ_ERR_CUDA;
 }

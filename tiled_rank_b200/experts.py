@@ -34,8 +34,8 @@ So that no gradient is lost unseen, a product with an operand that requires one 
 ValueError while gradients are enabled: make it under ``torch.no_grad()`` or in a
 ``torch.autograd.Function``.  (The quantisers take such tensors; their results are
 steps, without a gradient.)  Tensors that do not fit raise ValueError, and TileQError
-what the library refuses (a stride or an address that is no multiple of 16 bytes),
-before anything is launched.
+what the library refuses (a stride or an address that is no multiple of 16 bytes, a
+result that shares memory with an operand), before anything is launched.
 """
 from __future__ import annotations
 
