@@ -421,3 +421,44 @@ def test_results_beside_and_over_operands(tq):
         with pytest.raises(tq.TileQError):
             call()
     assert torch.equal(x, keep)
+
+
+@pytest.mark.parametrize("call", ["grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw", "fp8_quantize",
+                                  "fp8_quantize_weights", "fp8_gemm"])
+@pytest.mark.parametrize("as_int", [False, True])
+def test_operands_dropped_while_another_stream_reads_them(tq, call, as_int):
+    """The memory of operands that the caller drops after a call on another stream is not handed out before it has run:
+    new tensors of their sizes lie elsewhere, and writing them changes no result."""
+    import torch
+    counts = [300, 212]
+    x, dy, w, off = _make(counts, 512, 1024, torch.bfloat16, seed=31)
+    xq, xs = tq.fp8_quantize(x)
+    wq, ws = tq.fp8_quantize_weights(w)
+    given = {"grouped_gemm": (x, w, off), "grouped_gemm_dx": (dy, w, off), "grouped_gemm_dw": (x, dy, off),
+             "fp8_quantize": (x,), "fp8_quantize_weights": (w,), "fp8_gemm": (xq, xs, wq, ws, off)}[call]
+    f = getattr(tq, call)
+    want = f(*given)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1000)
+    f(*given, stream=s)
+    # room for all that is made below: asking the driver for memory would wait for the GPU
+    room = [torch.empty_like(t) for t in given for _ in range(4)]
+    del room
+    torch.cuda.synchronize()
+    tmp = [t.clone() for t in given]
+    at = {t.data_ptr() for t in tmp}
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)           # some 50 ms in front of the call
+    got = f(*tmp, stream=s.cuda_stream if as_int else s)
+    del tmp
+    done = s.record_event()
+    again = [torch.empty_like(t) for t in given for _ in range(2)]
+    assert not done.query()
+    assert not at & {t.data_ptr() for t in again}
+    for t in again:
+        t.view(torch.uint8).fill_(0)
+    torch.cuda.synchronize()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+        assert torch.equal(a.float(), b.float())

@@ -25,9 +25,11 @@ the product is dense.
 
 Rows outside the offsets' range belong to no expert: a given ``out`` keeps them,
 a new one leaves them unset.  Calls are asynchronous on ``stream`` (the current
-stream of the tensors' device by default), hold no state from one to the next
-and can be captured into a CUDA graph (after one call on that device outside of a
-graph, which allocates its status word).
+stream of the tensors' device by default; the caller orders another one behind the
+work that fills the tensors, and may drop them once the call has returned; a new
+result belongs to ``stream``).  They hold no state from one to the next and can be
+captured into a CUDA graph (after one call on that device outside of a graph, which
+allocates its status word).
 
 Autograd does not record them: a backward pass calls the gradients' products itself.
 So that no gradient is lost unseen, a product with an operand that requires one raises
@@ -72,9 +74,10 @@ def expert_status(device="cuda") -> int:
         return L.tileq_device_status((_status_words.get(index) or _status_word(index))[0])
 
 
-def _elsewhere(index: int, stream, call):
+def _elsewhere(index: int, stream, call, *tensors):
     """call() with device `index` and the given stream (or the device's own) current: where a call is not for the
-    current device's current stream.  New outputs belong to the stream they are made on."""
+    current device's current stream.  New outputs belong to the stream they are made on; the memory of the given
+    tensors is not handed out again before that stream has come past the call."""
     if stream is None:
         stream = torch.cuda.current_stream(index)
     elif isinstance(stream, int):
@@ -82,7 +85,11 @@ def _elsewhere(index: int, stream, call):
     if stream.device.index != index:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
     with torch.cuda.stream(stream):
-        return call()
+        result = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return result
 
 
 def _check(status: int, name: str):
@@ -177,7 +184,8 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
         raise ValueError(f"x has {I} columns, w expects {Iw}")
     off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype))
+        return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype),
+                          x, w, expert_offsets, out)
     y = _result(out, out_dtype, x.dtype, (P, O), x)
     ld_y = 0 if out is None else _rows(y, "out", index)[2]
     g = L.tileq_grouped(code, _CODE[y.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
@@ -197,7 +205,8 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
         raise ValueError(f"dy has {O} columns, w expects {Ow}")
     off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype))
+        return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype),
+                          dy, w, expert_offsets, out)
     dx = _result(out, out_dtype, dy.dtype, (P, I), dy)
     ld_x = 0 if out is None else _rows(dx, "out", index)[2]
     g = L.tileq_grouped(code, _CODE[dx.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
@@ -221,7 +230,8 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
         raise ValueError(f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
     off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype))
+        return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype),
+                          x, dy, expert_offsets, out)
     dw = _result(out, out_dtype, x.dtype, (E, O, I), x)
     ld_w, stride_w = (0, 0) if out is None else _weights(dw, "out", index)[3:]
     g = L.tileq_grouped(code, _CODE[dw.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
@@ -279,7 +289,8 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     at = _vector(rows, R, _I32, "rows", index)
     factor = _vector(row_scale, R, _F32, "row_scale", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: fp8_quantize(x, rows, swiglu, row_scale, out, scales))
+        return _elsewhere(index, stream, lambda: fp8_quantize(x, rows, swiglu, row_scale, out, scales),
+                          x, rows, row_scale, out, scales)
     q, shape = _quantised(out, (R, C), x), (-(-C // 128), R)
     if scales is None:
         s, ld_s = x.new_empty(shape, dtype=_F32), 0
@@ -304,7 +315,7 @@ def fp8_quantize_weights(w, out=None, scales=None, stream=None):
     index = w.get_device()
     E, O, I, ld_w, stride_w = _weights(w, "w", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: fp8_quantize_weights(w, out, scales))
+        return _elsewhere(index, stream, lambda: fp8_quantize_weights(w, out, scales), w, out, scales)
     q, shape = _quantised(out, (E, O, I), w), (E, -(-O // 128), -(-I // 128))
     ld_q, stride_q = _weights(q, "out", index)[3:]
     if scales is None:
@@ -348,7 +359,8 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
     _scales(ws, blocks, index, "ws")
     off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
-        return _elsewhere(index, stream, lambda: fp8_gemm(xq, xs, wq, ws, expert_offsets, out, out_dtype))
+        return _elsewhere(index, stream, lambda: fp8_gemm(xq, xs, wq, ws, expert_offsets, out, out_dtype),
+                          xq, xs, wq, ws, expert_offsets, out)
     y = _result(out, out_dtype, torch.bfloat16, (P, O), xq)
     ld_y = 0 if out is None else _rows(y, "out", index)[2]
     g = L.tileq_grouped(L.TILEQ_DT_E4M3, _CODE[y.dtype], E, P, I, O, ld_x, ld_y, ld_w, stride_w, off)
