@@ -462,3 +462,37 @@ def test_operands_dropped_while_another_stream_reads_them(tq, call, as_int):
     torch.cuda.synchronize()
     for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
         assert torch.equal(a.float(), b.float())
+
+
+def test_autograd_sees_a_given_result_change(tq):
+    """A tensor that autograd has saved and a call then writes: its backward pass is refused, not computed from the new
+    values.  A call that is refused changes nothing."""
+    import torch
+    x, dy, w, off = _make([20, 12], 64, 64, torch.bfloat16)
+    xq, xs = tq.fp8_quantize(x)
+    wq, ws = tq.fp8_quantize_weights(w)
+    out = torch.ones(32, 64, device="cuda", dtype=torch.bfloat16)
+    given = [out, torch.ones_like(w), torch.ones(1, 32, device="cuda"), torch.ones(2, 1, 1, device="cuda")]
+    q, qw = torch.empty_like(xq), torch.empty_like(wq)
+    for t, call in ((out, lambda: tq.grouped_gemm(x, w, off, out=out)), (out, lambda: tq.grouped_gemm_dx(dy, w, off, out=out)),
+                    (out, lambda: tq.fp8_gemm(xq, xs, wq, ws, off, out=out)),
+                    (out, lambda: tq.grouped_gemm(x, w, off, out=out, stream=torch.cuda.Stream())),
+                    (given[1], lambda: tq.grouped_gemm_dw(x, dy, off, out=given[1])),
+                    (given[2], lambda: tq.fp8_quantize(x, scales=given[2])), (q, lambda: tq.fp8_quantize(x, out=q)),
+                    (given[3], lambda: tq.fp8_quantize_weights(w, scales=given[3])),
+                    (qw, lambda: tq.fp8_quantize_weights(w[0], out=qw[0]))):
+        leaf = torch.ones((), device="cuda", requires_grad=True)
+        loss = (leaf * t).sum() if t.dtype != torch.float8_e4m3fn else None
+        before = t._version
+        call()
+        torch.cuda.synchronize()
+        assert t._version > before
+        if loss is not None:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+    before = out._version
+    with pytest.raises(ValueError):
+        tq.grouped_gemm(x, w, off, out=out, out_dtype=torch.float32)
+    assert out._version == before
+    with torch.inference_mode():                 # no counter to move
+        tq.grouped_gemm(x, w, off, out=torch.empty_like(out))

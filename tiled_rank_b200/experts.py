@@ -50,6 +50,7 @@ from . import _lib as L
 _CODE = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16, torch.float32: L.TILEQ_DT_F32}
 _OPERAND = {torch.bfloat16: L.TILEQ_DT_BF16, torch.float16: L.TILEQ_DT_F16}
 _I32, _F32, _F8 = torch.int32, torch.float32, torch.float8_e4m3fn
+_written = torch.autograd.graph.increment_version  # a given result: autograd knows that a tensor it saved has changed
 _status_words: dict = {}   # of each device: the tensor and its address
 
 # A small product takes the GPU a few microseconds, so what a call costs on the host counts: the checks below read each
@@ -192,6 +193,8 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     word = _status_words.get(index) or _status_word(index)
     _check(L.lib().tileq_grouped_gemm(byref(g), x.data_ptr(), w.data_ptr(), y.data_ptr(), word[1], L.TILEQ_GROUPED_WS_BYTES,
                                       torch._C._cuda_getCurrentRawStream(index)), "tileq_grouped_gemm")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -214,6 +217,8 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
     _check(L.lib().tileq_grouped_gemm_dx(byref(g), dy.data_ptr(), w.data_ptr(), dx.data_ptr(), word[1],
                                          L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
            "tileq_grouped_gemm_dx")
+    if out is not None:
+        _written(out)
     return dx
 
 
@@ -239,6 +244,8 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
     _check(L.lib().tileq_grouped_gemm_dw(byref(g), x.data_ptr(), dy.data_ptr(), dw.data_ptr(), word[1],
                                          L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
            "tileq_grouped_gemm_dw")
+    if out is not None:
+        _written(out)
     return dw
 
 
@@ -299,6 +306,9 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out", index)[2], ld_s)
     _check(L.lib().tileq_fp8_quantize(byref(a), x.data_ptr(), q.data_ptr(), s.data_ptr(),
                                       torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize")
+    for t in (out, scales):
+        if t is not None:
+            _written(t)
     return q, s
 
 
@@ -326,6 +336,9 @@ def fp8_quantize_weights(w, out=None, scales=None, stream=None):
     g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
     _check(L.lib().tileq_fp8_quantize_weights(byref(g), w.data_ptr(), q.data_ptr(), ld_q, stride_q, s.data_ptr(),
                                               torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize_weights")
+    for t in (out, scales):
+        if t is not None:
+            _written(t)
     return q, s
 
 
@@ -368,4 +381,6 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
     _check(L.lib().tileq_fp8_gemm(byref(g), xq.data_ptr(), xs.data_ptr(), ld_xs, wq.data_ptr(), ws.data_ptr(), y.data_ptr(),
                                   word[1], L.TILEQ_GROUPED_WS_BYTES, torch._C._cuda_getCurrentRawStream(index)),
            "tileq_fp8_gemm")
+    if out is not None:
+        _written(out)
     return y
