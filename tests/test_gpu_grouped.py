@@ -496,3 +496,15 @@ def test_autograd_sees_a_given_result_change(tq):
     assert out._version == before
     with torch.inference_mode():                 # no counter to move
         tq.grouped_gemm(x, w, off, out=torch.empty_like(out))
+
+
+@pytest.mark.parametrize("P", [0, 1, 70, 1500])
+def test_one_expert_without_offsets(tq, P):
+    import torch
+    x, dy, w, off = _make([P], 136, 72, torch.bfloat16, seed=P)
+    for f, a, b in ((tq.grouped_gemm, x, w), (tq.grouped_gemm_dx, dy, w), (tq.grouped_gemm_dw, x, dy)):
+        want = f(a, b, off)
+        assert torch.equal(f(a, b, None), want) and torch.equal(f(a, b, None, stream=torch.cuda.current_stream()), want)
+    for f, a in ((tq.grouped_gemm, x), (tq.grouped_gemm_dx, dy)):
+        with pytest.raises(ValueError, match="2 experts need expert_offsets"):
+            f(a, torch.cat([w, w]), None)

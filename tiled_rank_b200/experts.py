@@ -10,6 +10,8 @@ fp16 and fp32)::
     dx = grouped_gemm_dx(dy, w, offsets)      # dx[p] = W_e^T dy[p]
     dw = grouped_gemm_dw(x, dy, offsets)      # dW_e  = sum_p dy[p] x[p]^T
 
+With ``None`` for the offsets there is one expert, of every row.
+
 In 8 bits, with e4m3 values and an fp32 scale for every 128 columns of a row and
 every 128 x 128 block of a weight matrix::
 
@@ -151,6 +153,13 @@ def _vector(t, n: int, dtype, name: str, index: int) -> int:
     return t.data_ptr()
 
 
+def _offsets(t, E: int, index: int) -> int:
+    """Pointer of the experts' offsets, 0 for none: one expert has every row."""
+    if t is None and E != 1:
+        raise ValueError(f"{E} experts need expert_offsets")
+    return _vector(t, E + 1, _I32, "expert_offsets", index)
+
+
 def _result(out, out_dtype, default, shape, like: torch.Tensor) -> torch.Tensor:
     """The given result, checked, or a new one."""
     if out is None:
@@ -183,7 +192,7 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     E, O, Iw, ld_w, stride_w = _weights(w, "w", index)
     if I != Iw:
         raise ValueError(f"x has {I} columns, w expects {Iw}")
-    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    off = _offsets(expert_offsets, E, index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype),
                           x, w, expert_offsets, out)
@@ -206,7 +215,7 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
     E, Ow, I, ld_w, stride_w = _weights(w, "w", index)
     if O != Ow:
         raise ValueError(f"dy has {O} columns, w expects {Ow}")
-    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    off = _offsets(expert_offsets, E, index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype),
                           dy, w, expert_offsets, out)
@@ -230,10 +239,10 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
     Py, O, ld_y = _rows(dy, "dy", index)
     if P != Py:
         raise ValueError(f"x has {P} rows, dy {Py}")
-    E = expert_offsets.numel() - 1
+    E = 1 if expert_offsets is None else expert_offsets.numel() - 1
     if not 1 <= E <= L.TILEQ_GROUPED_MAX_E:
         raise ValueError(f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
-    off = _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
+    off = _offsets(expert_offsets, E, index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype),
                           x, dy, expert_offsets, out)
