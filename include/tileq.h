@@ -412,9 +412,10 @@ tileq_status tileq_grouped_gemm_dw(const tileq_grouped *g, const void *x, const 
  * infinity becomes NaN: its scale and all its values.  Scales, row numbers and
  * row factors need the alignment of their elements only.
  * ------------------------------------------------------------------------- */
+#define TILEQ_FP8_MAX_C (65535 * 1024) /* widest rows that can be quantised (TILEQ_ERR_UNSUPPORTED) */
 typedef struct {
   int dtype;              /* x: TILEQ_DT_BF16, TILEQ_DT_F16 or TILEQ_DT_F32 */
-  int R, T, C;            /* rows of q, rows of x, columns of q (>= 1) */
+  int R, T, C;            /* rows of q, rows of x, columns of q (1..TILEQ_FP8_MAX_C) */
   int swiglu;             /* 1: x has 2C columns, gate then up, and v = silu(gate) * up in fp32; 0: v = x */
   const int32_t *rows;    /* device [R]: row r of q comes from row rows[r] of x (the gather of routed tokens; a
                              number outside [0, T) gives a row of zeros).  NULL: row r, T >= R */

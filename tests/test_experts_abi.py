@@ -138,6 +138,14 @@ def test_fp8_quantize_invalid(L, bad):
     assert _quant(L, **bad) == L.TILEQ_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("swiglu", [0, 1])
+@pytest.mark.parametrize("C", [65535 * 1024 + 1, (1 << 26) + 8, (1 << 31) - 1])
+def test_fp8_quantize_rows_too_wide(L, C, swiglu):
+    """A size that the kernel's grid cannot have is unsupported, not invalid."""
+    big = dict(x=A16, q=1 << 48, s=1 << 52)
+    assert _quant(L, C=C, swiglu=swiglu, **big) == L.TILEQ_ERR_UNSUPPORTED
+
+
 def test_fp8_quantize_no_rows(L):
     assert _quant(L, R=0, x=None, q=None, s=None) == L.TILEQ_OK
     assert L.lib().tileq_fp8_quantize(None, A16, A16, A16, None) == L.TILEQ_ERR_INVALID_ARG

@@ -293,7 +293,7 @@ tileq_status tileq_fp8_gemm(const tileq_grouped *g, const void *xq, const float 
 
 tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q, float *scales,
                                 tileq_stream_t stream) {
-  if (!p || p->R < 0 || p->T < 0 || p->C < 1 || p->C > (1 << 26) || (p->swiglu & ~1)) return TILEQ_ERR_INVALID_ARG;
+  if (!p || p->R < 0 || p->T < 0 || p->C < 1 || (p->swiglu & ~1)) return TILEQ_ERR_INVALID_ARG;
   if (p->dtype != TILEQ_DT_BF16 && p->dtype != TILEQ_DT_F16 && p->dtype != TILEQ_DT_F32) return TILEQ_ERR_INVALID_ARG;
   if (p->ld_x < 0 || p->ld_q < 0 || p->ld_s < 0 || (!p->rows && p->T < p->R)) return TILEQ_ERR_INVALID_ARG;
   if (!aligned4(p->rows) || !aligned4(p->row_scale)) return TILEQ_ERR_INVALID_ARG;
@@ -302,7 +302,7 @@ tileq_status tileq_fp8_quantize(const tileq_fp8_rows *p, const void *x, void *q,
   if ((p->T > 1 && ld_x < width) || (p->R > 1 && ld_q < p->C) || ld_s < p->R) return TILEQ_ERR_INVALID_ARG;
   if (p->R == 0) return TILEQ_OK;
   if (!q || !scales || !aligned16(q) || !aligned4(scales) || (!x && p->T > 0) || !aligned16(x)) return TILEQ_ERR_INVALID_ARG;
-  if (div_up(p->C, 1024) > 65535) return TILEQ_ERR_UNSUPPORTED;
+  if (p->C > TILEQ_FP8_MAX_C) return TILEQ_ERR_UNSUPPORTED;
   const int es = element_size(p->dtype);
   const Memory to = {q, p->C, p->R, p->R > 1 ? ld_q : 0}, to_scales = {scales, 4ll * p->R, div_up(p->C, 128), 4 * ld_s};
   const Memory from = {x, width * es, p->T, p->T > 1 ? ld_x * es : 0};

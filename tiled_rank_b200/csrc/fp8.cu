@@ -175,6 +175,7 @@ enum QuantKind { Q_PLAIN = 0, Q_FACTOR = 1, Q_SWIGLU = 2 };
 constexpr int kQRows = 8;    // rows of a CTA, a warp each
 constexpr int kQCols = 1024; // columns of a CTA: four 16-byte loads a lane, issued before the first is used
 constexpr int kQU = kQCols / 256;
+static_assert(TILEQ_FP8_MAX_C == 65535 * kQCols, "the grid's second extent");
 
 // A warp's 1024 columns of a row, 16 lanes a block of 128.  x, up: this lane's first value of the gate (or the row)
 // and of the up projection; n: values from this lane's first column to the end of the row.

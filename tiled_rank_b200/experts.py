@@ -289,7 +289,7 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     """Rows in e4m3 with a scale for every 128 columns: (q [R, C], scales [ceil(C / 128), R]).
 
     x [T, C] (swiglu: [T, 2C], gate then up, of which silu(gate) * up is quantised) in bf16, fp16
-    or fp32.  rows: int32 [R], the row of x of each row of q (outside [0, T): zeros); without it
+    or fp32, C up to 65535 * 1024.  rows: int32 [R], the row of x of each row of q (outside [0, T): zeros); without it
     R = T.  row_scale: fp32 [R], a factor of each row of q.
     """
     code = _CODE.get(x.dtype)
