@@ -2,7 +2,7 @@
 import pytest
 
 from experts_util import (assert_within, block_scale, dequant_rows, dequant_weights, fp8_terms, offsets_of,
-                          ref_forward, ref_quant_rows, ref_quant_weights)
+                          ref_forward, ref_quant_rows, ref_quant_weights, round_e4m3)
 
 pytestmark = pytest.mark.gpu
 
@@ -152,6 +152,87 @@ def test_swiglu_rows(tq, R, C, dtype):
         top = h[:, 128 * b:128 * (b + 1)].abs().amax(1)
         lo, hi = block_scale(top * (1 - eps)), block_scale(top * (1 + eps))
         assert ((s[b].double() == lo) | (s[b].double() == hi)).all()
+
+
+def _check_codes(q, s, h, eps):
+    """q and s of values that are h to within eps relative (and 2^-146: subnormal values' few last places): the exact
+    code wherever h / scale is further than that from a tie, one of its two neighbours inside; the exact scale wherever
+    the block's maximum is further than that from 448 times a power of two.  Returns how many codes had to be exact."""
+    import torch
+    exact = 0
+    for b in range(s.shape[0]):
+        at = slice(128 * b, 128 * (b + 1))
+        part, sc = h[:, at], s[b].double()
+        top = part.abs().amax(1)
+        lo, hi = block_scale(top * (1 - eps)), block_scale(top * (1 + eps))
+        assert ((sc == lo) | (sc == hi)).all()
+        v, off = part / sc[:, None], eps * part.abs() / sc[:, None] + 2.0 ** -146 / sc[:, None]
+        below, above = (round_e4m3((v - off).clamp(-448, 448)), round_e4m3((v + off).clamp(-448, 448)))
+        got = q[:, at].float().double()
+        assert ((got == below) | (got == above)).all()
+        exact += int((below == above).sum())
+    return exact
+
+
+# Values in fp32: expf is within 2 units of 2^-23 (CUDA's bound), e in silu = g e / (1 + e) enters with a factor of at
+# most 1; 1 + e and g e are rounded (2^-24 each), the quotient is within 2 units, and two more products are rounded
+SWIGLU_EPS = 2.0 ** -20      # 6 * 2^-23, rounded up
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_swiglu_codes(tq, dtype, gathered):
+    """A million values: 2^-12 of error in the arithmetic would change thousands of codes."""
+    import torch
+    r, T, C = _rng(17), 512, 2048
+    x = r(T, 2 * C).to(getattr(torch, dtype)) * 3
+    rows = None
+    if gathered:
+        rows = (torch.rand(T, generator=torch.Generator("cuda").manual_seed(5), device="cuda") * (T + 6) - 3).to(torch.int32)
+    w = r(T).abs() + 0.1
+    q, s = tq.fp8_quantize(x, rows=rows, swiglu=True, row_scale=w)
+    at, live = (torch.arange(T, device="cuda"), None) if rows is None else (rows.clamp(0, T - 1).long(), (rows >= 0) & (rows < T))
+    g, u = x[at].double().chunk(2, 1)
+    h = g * torch.sigmoid(g) * u * w.double()[:, None]
+    if live is not None:
+        h[~live] = 0
+        assert (s[:, ~live] == 1).all()
+    assert _check_codes(q, s, h, SWIGLU_EPS) > 0.999 * h.numel()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_swiglu_next_to_ties_and_borders(tq, dtype):
+    """Row factors that put a value 2^-18 to either side of a tie, or the block's maximum as far from 448 * 2^k: those
+    codes and scales are decided, as the arithmetic is within 2^-20."""
+    import torch
+    r, R, C = _rng(23), 4096, 128
+    x = (r(R, 2 * C) * 2).to(getattr(torch, dtype))
+    g, u = x.double().chunk(2, 1)
+    h = g * torch.sigmoid(g) * u
+    top = h.abs().amax(1)
+    # the largest value below half of the maximum that is far enough from zero, to be placed on 1.0625 * 2^m
+    mid = torch.where(h.abs() < top[:, None] / 2, h.abs(), torch.zeros_like(h)).amax(1)
+    assert (mid > top / 64).all()
+    side = 1 + torch.sign(r(R)).double() * 2.0 ** -18
+    two = torch.exp2((r(R) * 20).round().double())
+    for w in (448 * two / top * side, 1.0625 * two / mid * side):
+        w = w.float()
+        q, s = tq.fp8_quantize(x, swiglu=True, row_scale=w)
+        hw = h * w.double()[:, None]
+        assert _check_codes(q, s, hw, SWIGLU_EPS) > 0.999 * h.numel()
+
+
+def test_swiglu_of_tiny_values(tq):
+    """Results below the normal range of fp32: nothing is flushed to zero before the block's scale of 2^-126."""
+    import torch
+    r = _rng(29)
+    x = torch.cat([r(64, 256) * 1e-20, r(64, 256) * torch.logspace(-20, -24, 64, device="cuda")[:, None]], 1).float()
+    q, s = tq.fp8_quantize(x, swiglu=True)
+    g, u = x.double().chunk(2, 1)
+    _check_codes(q, s, g * torch.sigmoid(g) * u, SWIGLU_EPS)
+    # row k's largest value is some 2.5e-40 * 10^(-k / 16); codes other than zero start at half of 2^-9 * 2^-126, so that
+    # the first 22 rows or so have some
+    assert (s == 2.0 ** -126).any() and (q.float() != 0).any(1).sum() >= 16
 
 
 def test_swiglu_far_values(tq):
