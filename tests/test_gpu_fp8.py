@@ -258,6 +258,63 @@ def test_weights(tq, E, O, I, dtype):
     assert torch.equal(s0, s[0]) and _same(q0, rq[0])
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("C", [400, 1024, 2056, 333])
+@pytest.mark.parametrize("factor", [False, True])
+def test_non_finite_rows_of_every_type(tq, dtype, C, factor):
+    """One NaN or infinity anywhere makes its block NaN and leaves the row's others alone: 16-bit rows have a path of
+    their own, and a block is the first or the second of a pair."""
+    import torch
+    dt = getattr(torch, dtype)
+    blocks = -(-C // 128)
+    x = _rng(C)(6 * blocks, C).to(dt)
+    for b in range(blocks):
+        for j, v in enumerate((float("nan"), float("inf"), float("-inf"), torch.finfo(dt).max, -torch.finfo(dt).max, 0.0)):
+            x[6 * b + j, min(128 * b + 17 * j + 3, C - 1)] = v
+    w = torch.full((x.shape[0],), 0.5, device="cuda") if factor else None
+    q, s = tq.fp8_quantize(x, row_scale=w)
+    rq, rs = ref_quant_rows(x.double() * (0.5 if factor else 1.0))
+    assert torch.equal(s.isnan(), rs.isnan()) and torch.equal(s.nan_to_num().double(), rs.nan_to_num())
+    for b in range(blocks):
+        at = slice(128 * b, 128 * (b + 1))
+        bad = s[b].isnan()
+        assert int(bad.sum()) == 3
+        assert q[bad][:, at].float().isnan().all() and _same(q[~bad][:, at], rq[~bad][:, at])
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+@pytest.mark.parametrize("C", [256, 1000, 1027])
+def test_factors_of_other_types(tq, C, dtype):
+    import torch
+    x = _rng(C)(37, C).to(getattr(torch, dtype))
+    f = torch.exp(_rng(C + 1)(37))
+    q, s = tq.fp8_quantize(x, row_scale=f)
+    rq, rs = ref_quant_rows((x.float() * f[:, None]).double())       # one fp32 rounding, as the kernel's
+    assert torch.equal(s.double(), rs) and _same(q, rq)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("O,I,pad", [(200, 520, 8), (130, 260, 3), (256, 1024, 16), (1, 37, 1)])
+def test_weights_strided_and_into_given_arrays(tq, O, I, pad, dtype):
+    """Weights inside a larger array, quantised into a larger array, with blocks that are not finite."""
+    import torch
+    E, dt = 3, getattr(torch, dtype)
+    base = _rng(I)(E, O + 2, I + pad).to(dt)
+    w = base[:, :O, :I]
+    w[1, 0, 0], w[2, O - 1, I - 1] = float("nan"), float("inf")
+    big = torch.full((E, O + 1, I + 2 * pad), 3.0, device="cuda").to(torch.float8_e4m3fn)
+    sc = torch.full((E + 1, -(-O // 128), -(-I // 128)), -1.0, device="cuda")
+    q, s = tq.fp8_quantize_weights(w, out=big[:, :O, :I], scales=sc[:E])
+    assert q.data_ptr() == big.data_ptr() and s.data_ptr() == sc.data_ptr()
+    rq, rs = ref_quant_weights(torch.where(torch.isfinite(w), w, torch.zeros_like(w)).double())
+    bad = torch.zeros_like(s, dtype=torch.bool)
+    bad[1, 0, 0] = bad[2, -1, -1] = True
+    at = bad.repeat_interleave(128, 1).repeat_interleave(128, 2)[:, :O, :I]
+    assert torch.equal(s.isnan(), bad) and torch.equal(q.float().isnan(), at)
+    assert torch.equal(s[~bad].double(), rs[~bad]) and torch.equal(q.float().double()[~at], rq[~at])
+    assert (big[:, O:].float() == 3).all() and (big[:, :, I:].float() == 3).all() and (sc[E:] == -1).all()
+
+
 # ------------------------------------------------------------------ products
 def _operands(counts, I, O, seed=0, first=0, behind=0):
     """e4m3 operands with scales of any value, not powers of two."""
@@ -400,3 +457,19 @@ def test_same_bits_in_a_graph(tq):
     graph.replay()
     q, s = tq.fp8_quantize(x, rows=rows)
     assert torch.equal(out, tq.fp8_gemm(q, s, wq, ws, off))
+
+
+@pytest.mark.parametrize("out_dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("O,pad", [(1290, 1), (1291, 1), (1290, 2), (1304, 8), (1312, 16), (1237, 3)])
+def test_wide_tiles_of_every_type_and_stride(tq, O, pad, out_dtype):
+    """Experts of many rows, so that the wide tiles are taken: every result type, and rows that allow stores of one, two,
+    eight or sixteen values.  What lies around the results, and other experts' NaN, stays where it is."""
+    import torch
+    dt, I = getattr(torch, out_dtype), 656
+    xq, xs, wq, ws, off = _operands(LONG, I, O, seed=O, first=4, behind=5)
+    ws = ws * 1e-3                       # results inside fp16's range
+    xs[:, :4], xs[:, -5:] = float("nan"), float("nan")
+    P = xq.shape[0]
+    out = torch.full((P, O + pad), 9.0, dtype=dt, device="cuda")
+    y = _check(tq, xq, xs, wq, ws, off, "wide", out=out[:, :O])
+    assert y.dtype == dt and (out[:, O:] == 9).all() and (out[:4] == 9).all() and (out[-5:] == 9).all()

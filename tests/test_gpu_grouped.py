@@ -508,3 +508,32 @@ def test_one_expert_without_offsets(tq, P):
     for f, a in ((tq.grouped_gemm, x), (tq.grouped_gemm_dx, dy)):
         with pytest.raises(ValueError, match="2 experts need expert_offsets"):
             f(a, torch.cat([w, w]), None)
+
+
+@pytest.mark.parametrize("out_dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("d_in,d_out,pad", [(1300, 1290, 1), (1300, 1290, 2), (1288, 1304, 8), (1296, 1312, 16), (1111, 1237, 3)])
+def test_wide_tiles_of_every_type_and_stride(tq, d_in, d_out, pad, dtype, out_dtype):
+    """Experts of many rows, so that the wide tiles are taken, into results inside larger arrays: every result type, and
+    rows that allow stores of one, two, eight or sixteen values.  What lies around the results keeps its value."""
+    import torch
+    dt, out_dt, counts = getattr(torch, dtype), getattr(torch, out_dtype), LONG
+    P, E, q = sum(counts) + 9, len(counts), lambda n: -(-n // 8) * 8
+    g = torch.Generator(device="cuda").manual_seed(d_in + pad)
+    rnd = lambda *s: (torch.randn(*s, generator=g, device="cuda") / 4).to(dt)  # noqa: E731
+    x, dy, w = rnd(P, q(d_in))[:, :d_in], rnd(P, q(d_out))[:, :d_out], rnd(E, d_out, q(d_in))[:, :, :d_in]
+    off = offsets_of(counts, 4, "cuda")
+    a, b = 4, 4 + sum(counts)
+    y, dx = (torch.full((P, n + pad), 9.0, dtype=out_dt, device="cuda") for n in (d_out, d_in))
+    dw = torch.full((E, d_out + pad, d_in + pad), 9.0, dtype=out_dt, device="cuda")
+    tq.grouped_gemm(x, w, off, out=y[:, :d_out])
+    tq.grouped_gemm_dx(dy, w, off, out=dx[:, :d_in])
+    tq.grouped_gemm_dw(x, dy, off, out=dw[:, :d_out, :d_in])
+    for got, (ref, mag), terms, what in ((y[:, :d_out], ref_forward(x, w, off), d_in, "y"),
+                                         (dx[:, :d_in], ref_dx(dy, w, off), d_out, "dx")):
+        assert_within(got[a:b], ref[a:b], mag[a:b], terms, what)
+    assert_within(dw[:, :d_out, :d_in], *ref_dw(x, dy, off), max(counts), "dw")
+    for t, n in ((y, d_out), (dx, d_in)):
+        assert (t[:, n:] == 9).all() and (t[:a] == 9).all() and (t[b:] == 9).all()
+    assert (dw[:, d_out:] == 9).all() and (dw[:, :, d_in:] == 9).all()
+    assert tq.expert_status() == 0
