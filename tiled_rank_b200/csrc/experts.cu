@@ -123,9 +123,11 @@ long long tile_count(const GroupedTile &t, GroupedMode mode, const tileq_grouped
 // The wide kernel (256 x 256 tiles of a pair of CTAs; fp8: 128 x 256 of one) needs experts with rows to fill its
 // columns and tiles to fill the GPU; else the narrow one (128 x 64 tiles).  Measured, us narrow / wide:
 //   fwd 8 x 4096 -> 14336:   16 rows an expert 154 / 158, 64 rows 175 / 165;   60 x 2048 -> 1408, 68 rows: 70 / 62
-//   dx  8 x 14336 -> 4096:   16 rows 145 / 140;   60 x 1408 -> 2048, 17 rows: 58.9 / 57.8
+//   dx  8 x 14336 -> 4096:   4 rows 138 / 134, 16 rows 145 / 140
+//   dx  60 x 1408 -> 2048:   3 rows 52.9 / 55.4, 5 rows 55.6 / 55.7, 7 rows 57.1 / 55.7, 17 rows 58.9 / 57.8
 //   fwd 1 x 4096 -> 1536:    256 rows (6 wide tiles) 15.1 / 16.6;   1 x 2048 -> 2048, 1024 rows (32) 19.0 / 11.7
-//   fp8 8 x 4096 -> 14336:   16 rows 88 / 91, 24 rows 99 / 93, 64 rows 153 / 96
+//   fp8 8 x 4096 -> 14336:   12 rows 85 / 90, 16 rows 88 / 91, 24 rows 99 / 93, 64 rows 153 / 96
+//   fp8 64 x 4096 -> 1536:   12 rows 80.1 / 77.9, 16 rows 79.7 / 79.1, 18 rows 83.0 / 78.8
 //   fp8 1 x 8192 -> 1024:    512 rows (16 wide tiles) 21.1 / 27.6, 1024 rows (32) 32.3 / 27.9
 //   fp8 1 x 4096 -> 1536:    256 rows (12 wide tiles) 14.8 / 16.2, 512 rows (24) 18.5 / 16.5
 //   dW  512 x 512, 256 rows: 1 expert (4 wide tiles) 5.7 / 6.9, 6 experts (24) 6.7 / 6.9, 60 experts (240) 25.8 / 16.7

@@ -7,8 +7,9 @@
 // A power of two, because the division is then exact and the only rounding is
 // the one to e4m3; a floating format loses no precision by it, only up to one
 // bit of its range below 2^-6.  Both kernels are one pass over the data: a block
-// stays in registers between its maximum and its rounding, and what bounds them
-// is memory (2 or 4 bytes in, 1 byte out per value).
+// stays in registers between its maximum and its rounding.  Plain rows and weights
+// are bounded by memory (2 or 4 bytes in, 1 byte out per value), gathered rows by
+// L2's traffic to the SMs and the ALUs, SwiGLU by the instructions issued.
 #include "fp8.cuh"
 #include "kernels.cuh"
 
@@ -257,10 +258,13 @@ __device__ __forceinline__ void quant_part(const char *x, const char *up, uint8_
 }
 
 // One CTA per eight rows x 1024 columns, columns in the outer order: a slice of x that many rows are gathered from
-// stays in L2.  131072 gathered bf16 rows of 4096: 168 us, 0.69 GB through HBM (63 % of measured) and 1.6 GB between L2
-// and the SMs, the ALUs at 78 %; hence the 16-bit maxima and the path for whole parts without any check.  8192 rows of
-// 28672 without a gather: 113 us, 6.3 TB/s.  (Persistent CTAs with the next item's loads in flight: 276 us against 195
-// for one item a CTA at the time, as their registers leave a third of the warps; a warp for eight rows: 175 against 168.)
+// stays in L2.  131072 gathered bf16 rows of 4096: 168 us in a captured run of calls (181 with inputs that change),
+// 0.69 GB through HBM (63 % of measured) and 1.6 GB between L2 and the SMs, the ALUs at 78 %; hence the 16-bit maxima
+// and the path for whole parts without any check.  8192 rows of 28672 without a gather: 113 us, 6.3 TB/s.  SwiGLU of
+// 8192 bf16 rows of 14336: 119 us for 0.59 GB (91 us at the measured rate), 76 % of the issue slots busy with half of
+// the warps that would fit (64 registers).  (Persistent CTAs with the next item's loads in flight: 276 us against 195
+// for one item a CTA at the time, as their registers leave a third of the warps; a warp for eight rows: 175 against
+// 168.)
 // The scales of eight rows leave together: neighbouring rows are neighbours in a scale row, and single 4-byte
 // stores would each cost a 32-byte sector.
 // VEC: the width is a multiple of 8 and rows start at 16 (8, of q) bytes.
@@ -302,7 +306,8 @@ __global__ void __launch_bounds__(kQRows * 32, quant_ctas<DT, KIND>()) quant_row
   }
 }
 
-// One CTA per 128 x 128 block, 64 values a thread.  8 x 14336 x 4096 in bf16: 217 us, 6.5 TB/s.
+// One CTA per 128 x 128 block, 64 values a thread (fp32 ones spill 4 bytes of them).  8 x 14336 x 4096 in bf16: 217 us,
+// 6.5 TB/s.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) quant_weights_kernel(const QuantWeightsArgs P) {
   __shared__ uint32_t top[8];

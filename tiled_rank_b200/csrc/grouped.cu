@@ -13,7 +13,8 @@
 // Weights on the lanes, so that the ragged dimension (the rows of an expert) is
 // the MMA's N, which takes any multiple of 16 or 32 at run time: a short last
 // tile costs its own columns only.  The epilogue stores a column's 32 lanes as
-// one 64- or 128-byte run of an output row in every mode.
+// one 64- or 128-byte run of an output row in every mode (but for the wide fp8
+// kernel below, where a thread stores a row of its own in pieces of 32 bytes).
 //
 // One persistent CTA per SM (CG = 1) or a pair of CTAs on neighbouring SMs that
 // share one MMA of 256 lanes (CG = 2: each CTA loads its own 128 rows of A and
@@ -45,7 +46,7 @@
 //   64 x 4096 -> 1536, 131072 rows           1.13 ms at full clocks, tensor cores,
 //                                            1460 TFLOP/s; 1.35 to 1.43 ms (1150 to
 //                                            1220) under the power limit
-//   gradient of 8192 rows, 60 experts        76 us    memory, 80 % of measured
+//   gradient of 8192 rows, 60 experts        88 us    memory, 69 % of measured (76 us in a captured run of calls)
 //   dW of 8192 rows, 8 x 14336 x 4096        0.72 ms at full clocks, 0.80 to 0.84 at the limit
 //   fp8, 64 x 4096 -> 1536, 128 rows         64 us    memory, 90 % of measured
 //   fp8, 8192 rows, 8 x 14336 -> 4096        0.46 ms at full clocks, 2080 TFLOP/s (even rows): the fold
@@ -55,7 +56,16 @@
 // 1170 (8 x 14336 x 4096, 1024 rows each).
 // The fold is why fp8 wide tiles stay at half of the tensor cores' rate: without
 // its FMAs a 2048 x 5632 x 2048 product took 25.5 us instead of 34.9, without its
-// TMEM reads 30.8.  (Pairs of CTAs and sixteen fold warps were no faster.)
+// TMEM reads 30.8; the sharing of a last round's tiles, which came later, brought
+// the whole to 32.  (Pairs of CTAs and sixteen fold warps were no faster.)  Its 224
+// registers a fold warp spill 20 bytes a thread.
+// An accumulator goes back to the issuer by a relaxed arrival.  Tensor memory is no
+// part of what release and acquire order: its accesses are ordered by wait::ld and
+// the fences tcgen05.fence::before_thread_sync and ::after_thread_sync on either
+// side of the arrival and of the wait that sees it, and nothing else is handed over
+// with it.  (With release the arrival also waits for the thread's own stores: dW of
+// 512 rows, 8 x 4096 x 1536, 50.6 us instead of 39.6 side by side, 8 x 14336 -> 4096
+// in fp8 786 instead of 715.)
 // Every wait is bounded and reports TILEQ_ERR_TIMEOUT.
 #include "grouped.cuh"
 
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(G::THREADS, 1) grouped_kernel(const __grid_con
   auto stage_a = [&](int s) { return smem + s * G::STAGE; };
   auto stage_b = [&](int s) { return smem + s * G::STAGE + G::A_BYTES; };
 
-    if (threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     for (int s = 0; s < SQ; ++s) {
       mbar_init(&full[s], CG);
       mbar_init(&empty[s], PARTS);

@@ -106,7 +106,8 @@ __device__ __forceinline__ void store4_at(uint32_t cluster_addr, float a, float 
                : "memory");
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;\n" ::: "memory"); }
-// An arrival that orders tensor-memory reads only (after wait::ld and tcgen05.fence::before_thread_sync).
+// An arrival for tensor-memory reads alone, which wait::ld and tcgen05.fence::before_thread_sync in front of it order
+// with what follows the waiting thread's tcgen05.fence::after_thread_sync.  It hands over nothing else.
 __device__ __forceinline__ void arrive_relaxed_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
