@@ -100,13 +100,11 @@ def _check(status: int, name: str):
         raise L.TileQError(status, name)
 
 
-def _unrecorded(*tensors):
-    """No gradient may be lost silently: refuse what autograd would have to record."""
+def _unrecorded():
+    """An operand requires a gradient: no gradient may be lost silently, so refuse what autograd would have to record."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("autograd does not record this product, and an operand requires a gradient: call it "
-                                 "under torch.no_grad() or in a torch.autograd.Function")
+        raise ValueError("autograd does not record this product, and an operand requires a gradient: call it under "
+                         "torch.no_grad() or in a torch.autograd.Function")
 
 
 def _rows(t: torch.Tensor, name: str, index: int):
@@ -153,11 +151,11 @@ def _vector(t, n: int, dtype, name: str, index: int) -> int:
     return t.data_ptr()
 
 
-def _offsets(t, E: int, index: int) -> int:
-    """Pointer of the experts' offsets, 0 for none: one expert has every row."""
-    if t is None and E != 1:
+def _no_offsets(E: int) -> int:
+    """None for the offsets: one expert has every row."""
+    if E != 1:
         raise ValueError(f"{E} experts need expert_offsets")
-    return _vector(t, E + 1, _I32, "expert_offsets", index)
+    return 0
 
 
 def _result(out, out_dtype, default, shape, like: torch.Tensor) -> torch.Tensor:
@@ -186,13 +184,14 @@ def _operands(a: torch.Tensor, b: torch.Tensor) -> int:
 
 def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """y [P, d_out] with y[p] = W_e x[p]: x [P, d_in], w [E, d_out, d_in]."""
-    _unrecorded(x, w, out)
+    if x.requires_grad or w.requires_grad or (out is not None and out.requires_grad):
+        _unrecorded()
     code, index = _operands(x, w), x.get_device()
     P, I, ld_x = _rows(x, "x", index)
     E, O, Iw, ld_w, stride_w = _weights(w, "w", index)
     if I != Iw:
         raise ValueError(f"x has {I} columns, w expects {Iw}")
-    off = _offsets(expert_offsets, E, index)
+    off = _no_offsets(E) if expert_offsets is None else _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm(x, w, expert_offsets, out, out_dtype),
                           x, w, expert_offsets, out)
@@ -209,13 +208,14 @@ def grouped_gemm(x, w, expert_offsets, out=None, out_dtype=None, stream=None):
 
 def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None):
     """dx [P, d_in] with dx[p] = W_e^T dy[p]: dy [P, d_out], w [E, d_out, d_in]."""
-    _unrecorded(dy, w, out)
+    if dy.requires_grad or w.requires_grad or (out is not None and out.requires_grad):
+        _unrecorded()
     code, index = _operands(dy, w), dy.get_device()
     P, O, ld_y = _rows(dy, "dy", index)
     E, Ow, I, ld_w, stride_w = _weights(w, "w", index)
     if O != Ow:
         raise ValueError(f"dy has {O} columns, w expects {Ow}")
-    off = _offsets(expert_offsets, E, index)
+    off = _no_offsets(E) if expert_offsets is None else _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dx(dy, w, expert_offsets, out, out_dtype),
                           dy, w, expert_offsets, out)
@@ -233,7 +233,8 @@ def grouped_gemm_dx(dy, w, expert_offsets, out=None, out_dtype=None, stream=None
 
 def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None):
     """dW [E, d_out, d_in] with dW_e = sum over the rows p of e of dy[p] x[p]^T, zeros for an expert without rows."""
-    _unrecorded(x, dy, out)
+    if x.requires_grad or dy.requires_grad or (out is not None and out.requires_grad):
+        _unrecorded()
     code, index = _operands(x, dy), x.get_device()
     P, I, ld_x = _rows(x, "x", index)
     Py, O, ld_y = _rows(dy, "dy", index)
@@ -242,7 +243,7 @@ def grouped_gemm_dw(x, dy, expert_offsets, out=None, out_dtype=None, stream=None
     E = 1 if expert_offsets is None else expert_offsets.numel() - 1
     if not 1 <= E <= L.TILEQ_GROUPED_MAX_E:
         raise ValueError(f"expert_offsets must hold 2 to {L.TILEQ_GROUPED_MAX_E + 1} values")
-    off = _offsets(expert_offsets, E, index)
+    off = _no_offsets(E) if expert_offsets is None else _vector(expert_offsets, E + 1, _I32, "expert_offsets", index)
     if stream is not None or torch.cuda.current_device() != index:
         return _elsewhere(index, stream, lambda: grouped_gemm_dw(x, dy, expert_offsets, out, out_dtype),
                           x, dy, expert_offsets, out)
@@ -315,9 +316,10 @@ def fp8_quantize(x, rows=None, swiglu=False, row_scale=None, out=None, scales=No
     a = L.tileq_fp8_rows(code, R, T, C, 1 if swiglu else 0, at, factor, ld_x, _rows(q, "out", index)[2], ld_s)
     _check(L.lib().tileq_fp8_quantize(byref(a), x.data_ptr(), q.data_ptr(), s.data_ptr(),
                                       torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize")
-    for t in (out, scales):
-        if t is not None:
-            _written(t)
+    if out is not None:
+        _written(out)
+    if scales is not None:
+        _written(scales)
     return q, s
 
 
@@ -345,9 +347,10 @@ def fp8_quantize_weights(w, out=None, scales=None, stream=None):
     g = L.tileq_grouped(code, 0, E, 0, I, O, 0, 0, ld_w, stride_w, 0)
     _check(L.lib().tileq_fp8_quantize_weights(byref(g), w.data_ptr(), q.data_ptr(), ld_q, stride_q, s.data_ptr(),
                                               torch._C._cuda_getCurrentRawStream(index)), "tileq_fp8_quantize_weights")
-    for t in (out, scales):
-        if t is not None:
-            _written(t)
+    if out is not None:
+        _written(out)
+    if scales is not None:
+        _written(scales)
     return q, s
 
 
@@ -357,7 +360,8 @@ def fp8_gemm(xq, xs, wq, ws, expert_offsets=None, out=None, out_dtype=None, stre
 
     Dense, without expert_offsets: wq [d_out, d_in], ws [ceil(d_out / 128), ceil(d_in / 128)].
     """
-    _unrecorded(xs, ws, out)
+    if xs.requires_grad or ws.requires_grad or (out is not None and out.requires_grad):
+        _unrecorded()
     if (wq.dim() == 2) != (expert_offsets is None):
         raise ValueError("a product by expert takes wq [E, d_out, d_in] and expert_offsets, a dense one wq [d_out, d_in]")
     if xq.dtype is not _F8 or wq.dtype is not _F8:
