@@ -537,3 +537,31 @@ def test_wide_tiles_of_every_type_and_stride(tq, d_in, d_out, pad, dtype, out_dt
         assert (t[:, n:] == 9).all() and (t[:a] == 9).all() and (t[b:] == 9).all()
     assert (dw[:, d_out:] == 9).all() and (dw[:, :, d_in:] == 9).all()
     assert tq.expert_status() == 0
+
+
+def test_a_captured_call_on_a_side_stream(tq):
+    """A graph whose calls run on a stream beside the capturing one, with operands that are made and dropped within it."""
+    import torch
+    x, dy, w, off = _make(LONG, 256, 512, torch.bfloat16, seed=41)
+    side, out = torch.cuda.Stream(), torch.empty(x.shape[0], 512, dtype=x.dtype, device="cuda")
+    wq, ws = tq.fp8_quantize_weights(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        twice = x * 2
+        side.wait_stream(torch.cuda.current_stream())
+        tq.grouped_gemm(twice, w, off, out=out, stream=side)
+        dw = tq.grouped_gemm_dw(twice, dy, off, stream=side)
+        q, s = tq.fp8_quantize(twice, stream=side)
+        y8 = tq.fp8_gemm(q, s, wq, ws, off, stream=side)
+        del twice, q, s
+        filler = [torch.zeros_like(x) for _ in range(3)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in (out, dw, y8):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, tq.grouped_gemm(x * 2, w, off)) and torch.equal(dw, tq.grouped_gemm_dw(x * 2, dy, off))
+        assert torch.equal(y8, tq.fp8_gemm(*tq.fp8_quantize(x * 2), wq, ws, off))
+        x.copy_(x.roll(1, 0))
+    del filler
